@@ -9,6 +9,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "loza_ssa.h"
@@ -22,6 +23,9 @@
 #include "merge.cuh"
 #include "backward.cuh"
 #include "hi_index.cuh"
+#include "page_plan.cuh"
+#include "norm_rope.cuh"
+#include "decode_paged_kv.cuh"
 
 namespace loza {
 namespace {
@@ -1405,3 +1409,5 @@ loza_status loza_ssa_decode_noalloc(const void* q, const void* k_cache, const vo
 }
 
 }  // extern "C"
+
+#include "paged_host.cuh"

@@ -1,0 +1,539 @@
+// paged_host.cuh - host side of the serving and training operators around the
+// attention: the page plan, the position rotation, the norm of query and key
+// heads with its gradient, and the decode over paged K and V pools. Included
+// by loza_ssa.cu, whose helpers (window checks, launch count) it uses.
+#pragma once
+
+#include <cmath>
+
+namespace loza {
+namespace {
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A kernel behind the one that writes what it reads (it waits for it itself).
+template <typename P>
+bool launch_after(void (*kernel)(P), dim3 grid, unsigned threads, cudaStream_t st, const P& prm) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, prm) == cudaSuccess;
+}
+
+// ---------------------------------------------------------------------------
+// Norm and rotation
+// ---------------------------------------------------------------------------
+int elt_size(int dtype) { return dtype == LOZA_FP32 ? 4 : 2; }
+
+// Shape checks that forward and backward share; fills everything but the task counts.
+loza_status nr_shape(NrShape* s, int64_t tokens, int32_t d, int32_t norm_dim, float eps, const int32_t* positions,
+                     const double* inv_freq, const loza_rope_params& r, int dtype) {
+  if (dtype != LOZA_BF16 && dtype != LOZA_FP16 && dtype != LOZA_FP32) return LOZA_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > INT32_MAX || d < 1 || norm_dim < 0 || norm_dim > d) return LOZA_ERR_INVALID_ARG;
+  if (d > 1024) return LOZA_ERR_UNSUPPORTED;
+  if (r.rope_dim < 0 || r.rope_dim % 2 != 0 || r.rope_offset < 0 || (int64_t)r.rope_offset + r.rope_dim > d)
+    return LOZA_ERR_INVALID_ARG;
+  if (r.interleaved != 0 && r.interleaved != 1) return LOZA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f)) return LOZA_ERR_INVALID_ARG;
+  if (r.rope_dim > 0 && tokens > 0 &&
+      (!positions || !inv_freq || !aligned_to(positions, 4) || !aligned_to(inv_freq, 8)))
+    return LOZA_ERR_INVALID_ARG;
+  *s = NrShape{};
+  s->d = d;
+  s->norm_dim = norm_dim;
+  s->rope_off = r.rope_offset;
+  s->half = r.rope_dim / 2;
+  s->interleaved = r.interleaved;
+  s->scale = r.scale;
+  s->sign = 1.f;
+  s->eps = eps;
+  s->inv_norm = norm_dim > 0 ? 1.f / (float)norm_dim : 0.f;
+  s->inv_freq = inv_freq;
+  s->positions = positions;
+  s->tokens = tokens;
+  return LOZA_OK;
+}
+
+bool nr_rows_ok(const void* x, int64_t stride, int heads, int d, int size) {
+  return x && aligned_to(x, size) && stride >= (int64_t)heads * d && stride < (int64_t(1) << 40);
+}
+
+// Largest vector (in elements) that every size, offset and stride allows: 16 bytes, or one element.
+int nr_vec(const NrShape& s, int size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> sizes) {
+  const int v = 16 / size;
+  if (s.d % v || s.norm_dim % v || s.rope_off % v || s.half % v) return 1;
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return 1;
+  for (int64_t n : sizes)
+    if (n % v) return 1;
+  return v;
+}
+
+// Tasks (pairs of vectors) of a row, and how many a lane takes; returns that number (NV).
+int nr_tasks(NrShape* s, int vec) {
+  s->nrope = s->half / vec;
+  s->npass = (s->d - 2 * s->half) / vec;
+  s->ntasks = s->nrope + (s->npass + 1) / 2;
+  int nv = vec == 1 ? 4 : 1;
+  while (nv * 32 < s->ntasks) nv = vec == 1 ? 16 : nv * 2;
+  s->lph = 1;
+  while (s->lph * nv < s->ntasks) s->lph *= 2;
+  return nv;
+}
+
+template <typename T, int VEC, int NV>
+bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
+  const int64_t grid = (p.s.tokens * p.parts + kNrWarps - 1) / kNrWarps;
+  const size_t smem = (size_t)kNrWarps * p.s.half * sizeof(float2);
+  norm_rope_kernel<T, VEC, NV><<<(unsigned)grid, kNrThreads, smem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+template <typename T, int VEC, int NV>
+bool nr_launch_bwd(const NrBwdParams& p, int ctas, cudaStream_t st) {
+  const size_t smem = (size_t)kNrWarps * (p.s.half * sizeof(float2) + p.s.norm_dim * sizeof(float));
+  norm_rope_backward_kernel<T, VEC, NV><<<(unsigned)ctas, kNrThreads, smem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess;
+}
+
+template <typename T>
+bool nr_fwd16(const NrFwdParams& p, int vec, int nv, cudaStream_t st) {
+  if (vec == 8) return nv == 1 ? nr_launch_fwd<T, 8, 1>(p, st) : nr_launch_fwd<T, 8, 2>(p, st);
+  return nv == 4 ? nr_launch_fwd<T, 1, 4>(p, st) : nr_launch_fwd<T, 1, 16>(p, st);
+}
+bool nr_fwd32(const NrFwdParams& p, int vec, int nv, cudaStream_t st) {
+  if (vec == 4)
+    return nv == 1   ? nr_launch_fwd<float, 4, 1>(p, st)
+           : nv == 2 ? nr_launch_fwd<float, 4, 2>(p, st)
+                     : nr_launch_fwd<float, 4, 4>(p, st);
+  return nv == 4 ? nr_launch_fwd<float, 1, 4>(p, st) : nr_launch_fwd<float, 1, 16>(p, st);
+}
+bool nr_fwd(const NrFwdParams& p, int dtype, int vec, int nv, cudaStream_t st) {
+  if (dtype == LOZA_BF16) return nr_fwd16<__nv_bfloat16>(p, vec, nv, st);
+  if (dtype == LOZA_FP16) return nr_fwd16<__half>(p, vec, nv, st);
+  return nr_fwd32(p, vec, nv, st);
+}
+
+template <typename T>
+bool nr_bwd16(const NrBwdParams& p, int vec, int nv, int ctas, cudaStream_t st) {
+  if (vec == 8) return nv == 1 ? nr_launch_bwd<T, 8, 1>(p, ctas, st) : nr_launch_bwd<T, 8, 2>(p, ctas, st);
+  return nv == 4 ? nr_launch_bwd<T, 1, 4>(p, ctas, st) : nr_launch_bwd<T, 1, 16>(p, ctas, st);
+}
+bool nr_bwd32(const NrBwdParams& p, int vec, int nv, int ctas, cudaStream_t st) {
+  if (vec == 4)
+    return nv == 1   ? nr_launch_bwd<float, 4, 1>(p, ctas, st)
+           : nv == 2 ? nr_launch_bwd<float, 4, 2>(p, ctas, st)
+                     : nr_launch_bwd<float, 4, 4>(p, ctas, st);
+  return nv == 4 ? nr_launch_bwd<float, 1, 4>(p, ctas, st) : nr_launch_bwd<float, 1, 16>(p, ctas, st);
+}
+bool nr_bwd(const NrBwdParams& p, int dtype, int vec, int nv, int ctas, cudaStream_t st) {
+  if (dtype == LOZA_BF16) return nr_bwd16<__nv_bfloat16>(p, vec, nv, ctas, st);
+  if (dtype == LOZA_FP16) return nr_bwd16<__half>(p, vec, nv, ctas, st);
+  return nr_bwd32(p, vec, nv, ctas, st);
+}
+
+// Warps per token of the forward: enough to give every SM 16 warps while
+// there are few tokens, never more than a token has row groups.
+int nr_parts(int64_t tokens, int64_t groups) {
+  const int64_t want = ((int64_t)sm_count() * 16 + tokens - 1) / tokens;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, groups, 64}));
+}
+
+constexpr int kNrBwdCtasPerSm = 4;
+int nr_bwd_max_ctas() { return sm_count() * kNrBwdCtasPerSm; }
+
+bool pool_page_ok(const loza_kv_pool& p) {
+  return p.num_pages >= 1 && p.page_size >= 1 && p.page_size <= 65536 && (p.page_size & (p.page_size - 1)) == 0 &&
+         (int64_t)p.num_pages * p.page_size <= INT32_MAX;
+}
+bool pool_strides_ok(int64_t page, int64_t row, int64_t head) {
+  const int64_t cap = int64_t(1) << 40;
+  return page >= 0 && row >= 0 && head >= 0 && page < cap && row < cap && head < cap;
+}
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// Paged K/V decode
+// ---------------------------------------------------------------------------
+int pkv_ctas() { return sm_count() * kPkvCtasPerSm; }
+
+bool pkv_shape_ok(int32_t n_heads, int32_t n_kv, int32_t d_qk, int32_t d_v) {
+  return n_heads >= 1 && n_kv >= 1 && n_heads % n_kv == 0 && n_kv <= 65535 && n_heads <= 65535 &&
+         ((d_qk == 64 && d_v == 64) || (d_qk == 128 && d_v == 128) || (d_qk == 192 && d_v == 128));
+}
+
+size_t pkv_part_o_bytes(int32_t d_v) { return (size_t)pkv_ctas() * 2 * kPkvHeads * d_v * sizeof(float); }
+size_t pkv_workspace_bytes(int32_t d_v) {
+  return pkv_part_o_bytes(d_v) + (size_t)pkv_ctas() * 2 * kPkvHeads * 2 * sizeof(float);
+}
+
+template <typename T, int DQK, int DV, int NT>
+loza_status pkv_launch(const PagedKvParams& p, cudaStream_t st) {
+  auto kernel = decode_paged_kv_kernel<T, DQK, DV, NT>;
+  constexpr int smem = PagedKvLayout<DQK, DV>::kSmem;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return LOZA_ERR_CUDA;
+  kernel<<<(unsigned)p.ctas, kPkvThreads, smem, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return LOZA_ERR_CUDA;
+  if (!launch_after(decode_paged_join_kernel<T, DV>, dim3(p.n_kv * p.chunks, p.batch), 128, st, p))
+    return LOZA_ERR_CUDA;
+  g_launches.fetch_add(2, std::memory_order_relaxed);
+  return LOZA_OK;
+}
+
+template <typename T>
+loza_status pkv_dispatch(const PagedKvParams& p, int d_qk, cudaStream_t st) {
+  const bool wide = p.chunk > 8;  // more than one tile of 8 query heads
+  if (d_qk == 64) return wide ? pkv_launch<T, 64, 64, 2>(p, st) : pkv_launch<T, 64, 64, 1>(p, st);
+  if (d_qk == 128) return wide ? pkv_launch<T, 128, 128, 2>(p, st) : pkv_launch<T, 128, 128, 1>(p, st);
+  return wide ? pkv_launch<T, 192, 128, 2>(p, st) : pkv_launch<T, 192, 128, 1>(p, st);
+}
+
+}  // namespace
+}  // namespace loza
+
+using namespace loza;
+
+extern "C" {
+
+loza_status loza_page_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t batch, const int32_t* free_pages,
+                           int32_t n_free, int32_t page_size, int32_t* block_table, int64_t bt_stride,
+                           int32_t max_pages, int64_t capacity, int32_t* cu_seqlens, int32_t* seqlens,
+                           int32_t* positions, int64_t* slots, int32_t* counts, loza_stream_t stream) {
+  if (batch < 1 || n_free < 0 || max_pages < 0 || capacity < 0 || capacity > INT32_MAX) return LOZA_ERR_INVALID_ARG;
+  if (page_size < 1 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return LOZA_ERR_INVALID_ARG;
+  if (!ctx_lens || !new_lens || !cu_seqlens || !seqlens || !counts) return LOZA_ERR_INVALID_ARG;
+  if ((n_free > 0 && !free_pages) || (max_pages > 0 && !block_table) || bt_stride < max_pages)
+    return LOZA_ERR_INVALID_ARG;
+  if (capacity > 0 && (!positions || !slots || !aligned16(positions) || !aligned16(slots)))
+    return LOZA_ERR_INVALID_ARG;
+  if (batch > kPlanMaxBatch) return LOZA_ERR_UNSUPPORTED;
+  PlanParams p{};
+  p.ctx = ctx_lens;
+  p.add = new_lens;
+  p.free_pages = free_pages;
+  p.table = block_table;
+  p.table_stride = bt_stride;
+  p.batch = batch;
+  p.max_pages = max_pages;
+  p.n_free = n_free;
+  p.page_shift = log2_of(page_size);
+  p.capacity = capacity;
+  p.cu = cu_seqlens;
+  p.seqlens = seqlens;
+  p.positions = positions;
+  p.slots = slots;
+  p.counts = counts;
+  const size_t smem = (size_t)(batch + 1) * 2 * sizeof(int);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem) != cudaSuccess)
+    return LOZA_ERR_CUDA;
+  // four tokens a thread; new pages are at most one a request more than tokens / page_size
+  const int64_t work = std::max<int64_t>((capacity + 3) / 4, batch);
+  const unsigned grid = (unsigned)std::max<int64_t>(
+      1, std::min<int64_t>((work + kPlanThreads - 1) / kPlanThreads, (int64_t)sm_count() * 2));
+  page_plan_kernel<<<grid, kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return cudaGetLastError() == cudaSuccess ? LOZA_OK : LOZA_ERR_CUDA;
+}
+
+loza_status loza_rope_frequencies(double theta, int32_t rope_dim, int32_t scaling, double factor, double original_max,
+                                  double beta_fast, double beta_slow, double* inv_freq, float* scale) {
+  if (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > 1024 || !inv_freq || !scale) return LOZA_ERR_INVALID_ARG;
+  if (!(theta > 1.0) || !std::isfinite(theta) || !(factor >= 1.0) || !std::isfinite(factor))
+    return LOZA_ERR_INVALID_ARG;
+  const int half = rope_dim / 2;
+  const double pi2 = 6.28318530717958647693;
+  *scale = 1.f;
+  if (scaling == LOZA_ROPE_NTK) {
+    if (rope_dim == 2) return LOZA_ERR_INVALID_ARG;  // its exponent dim / (dim - 2)
+    theta *= std::pow(factor, (double)rope_dim / (rope_dim - 2));
+  }
+  double low = 0, high = 0;
+  if (scaling == LOZA_ROPE_YARN) {
+    if (!(original_max >= 1.0) || !(beta_slow > 0.0) || !(beta_fast > beta_slow)) return LOZA_ERR_INVALID_ARG;
+    // the (fractional) pair index whose frequency makes `turns` turns over the original length, times two
+    auto column = [&](double turns) {
+      return rope_dim * std::log(original_max / (turns * pi2)) / (2 * std::log(theta));
+    };
+    low = std::max(std::floor(column(beta_fast)), 0.0);
+    high = std::min(std::ceil(column(beta_slow)), (double)rope_dim - 1);
+    *scale = factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  } else if (scaling != LOZA_ROPE_NONE && scaling != LOZA_ROPE_LINEAR && scaling != LOZA_ROPE_NTK) {
+    return LOZA_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < half; ++i) {
+    double f = std::pow(theta, -(double)i / half);
+    if (scaling == LOZA_ROPE_LINEAR) f /= factor;
+    if (scaling == LOZA_ROPE_YARN) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 0.001)));
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    inv_freq[i] = f;
+  }
+  return LOZA_OK;
+}
+
+loza_status loza_rope(const void* x, const int32_t* positions, const double* inv_freq, int64_t tokens,
+                      int32_t n_heads, int32_t d, int64_t x_row_stride, loza_rope_params rope, int32_t transposed,
+                      int32_t dtype, void* out, int64_t out_row_stride, loza_stream_t stream) {
+  NrFwdParams p{};
+  const loza_status rc = nr_shape(&p.s, tokens, d, 0, 0.f, positions, inv_freq, rope, dtype);
+  if (rc != LOZA_OK) return rc;
+  if (n_heads < 1 || n_heads > 65535 || (transposed != 0 && transposed != 1)) return LOZA_ERR_INVALID_ARG;
+  if (tokens == 0) return LOZA_OK;
+  const int size = elt_size(dtype);
+  if (!nr_rows_ok(x, x_row_stride, n_heads, d, size) || !nr_rows_ok(out, out_row_stride, n_heads, d, size))
+    return LOZA_ERR_INVALID_ARG;
+  if (x == out && x_row_stride != out_row_stride) return LOZA_ERR_INVALID_ARG;
+  if (x == out && rope.rope_dim == 0) return LOZA_OK;
+  if (transposed) p.s.sign = -1.f;
+  p.q.x = x;
+  p.q.x_stride = x_row_stride;
+  p.q.out = out;
+  p.q.out_stride = out_row_stride;
+  p.q.heads = n_heads;
+  const int vec = nr_vec(p.s, size, {x, out}, {x_row_stride, out_row_stride});
+  int nv = nr_tasks(&p.s, vec);
+  if (x == out) {  // in place: the rotated columns alone
+    p.s.npass = 0;
+    p.s.ntasks = p.s.nrope;
+    p.s.lph = 1;
+    while (p.s.lph * nv < p.s.ntasks) p.s.lph *= 2;
+  }
+  p.parts = nr_parts(tokens, (n_heads + 32 / p.s.lph - 1) / (32 / p.s.lph));
+  if (!nr_fwd(p, dtype, vec, nv, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return LOZA_OK;
+}
+
+loza_status loza_qk_norm_rope(const void* q, const void* k, const void* v, const int32_t* positions,
+                              const double* inv_freq, int64_t tokens, int32_t n_heads, int32_t n_kv_heads, int32_t d,
+                              int32_t d_v, int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                              const void* q_weight, const void* k_weight, int32_t norm_dim, float eps,
+                              loza_rope_params rope, int32_t dtype, void* q_out, int64_t q_out_row_stride,
+                              void* k_out, int64_t k_out_row_stride, const loza_kv_pool* pool, const int64_t* slots,
+                              loza_stream_t stream) {
+  NrFwdParams p{};
+  const loza_status rc = nr_shape(&p.s, tokens, d, norm_dim, eps, positions, inv_freq, rope, dtype);
+  if (rc != LOZA_OK) return rc;
+  if (n_heads < 0 || n_kv_heads < 0 || n_heads > 65535 || n_kv_heads > 65535 || n_heads + n_kv_heads < 1)
+    return LOZA_ERR_INVALID_ARG;
+  const int size = elt_size(dtype);
+  if ((q_weight || k_weight) && norm_dim < 1) return LOZA_ERR_INVALID_ARG;
+  if (!aligned_to(q_weight, size) || !aligned_to(k_weight, size)) return LOZA_ERR_INVALID_ARG;
+  if (pool) {
+    if (!pool_page_ok(*pool) || !pool->k || !aligned_to(pool->k, size) ||
+        !pool_strides_ok(pool->k_page_stride, pool->k_row_stride, pool->k_head_stride))
+      return LOZA_ERR_INVALID_ARG;
+    if (n_kv_heads < 1 || (tokens > 0 && (!slots || !aligned_to(slots, 8)))) return LOZA_ERR_INVALID_ARG;
+    if ((v != nullptr) != (pool->v != nullptr)) return LOZA_ERR_INVALID_ARG;
+    if (v && (d_v < 1 || d_v > 1024 || !aligned_to(pool->v, size) ||
+              !pool_strides_ok(pool->v_page_stride, pool->v_row_stride, pool->v_head_stride)))
+      return LOZA_ERR_INVALID_ARG;
+  } else if (v || slots) {
+    return LOZA_ERR_INVALID_ARG;  // values and slots are for the pool
+  }
+  if (n_kv_heads > 0 && !pool && !k_out) return LOZA_ERR_INVALID_ARG;
+  if (tokens == 0) return LOZA_OK;
+  if (n_heads > 0 &&
+      (!nr_rows_ok(q, q_row_stride, n_heads, d, size) || !nr_rows_ok(q_out, q_out_row_stride, n_heads, d, size)))
+    return LOZA_ERR_INVALID_ARG;
+  if (n_kv_heads > 0 && (!nr_rows_ok(k, k_row_stride, n_kv_heads, d, size) ||
+                         (k_out && !nr_rows_ok(k_out, k_out_row_stride, n_kv_heads, d, size))))
+    return LOZA_ERR_INVALID_ARG;
+  if (v && !nr_rows_ok(v, v_row_stride, n_kv_heads, d_v, size)) return LOZA_ERR_INVALID_ARG;
+  if ((n_heads > 0 && q == q_out && q_row_stride != q_out_row_stride) ||
+      (n_kv_heads > 0 && k == k_out && k_row_stride != k_out_row_stride))
+    return LOZA_ERR_INVALID_ARG;
+  if (n_heads > 0) {
+    p.q = NrSide{q, nullptr, q_weight, q_out, q_row_stride, 0, q_out_row_stride, n_heads, q == q_out && !q_weight};
+  }
+  if (n_kv_heads > 0) {
+    p.k = NrSide{k, nullptr, k_weight, k_out, k_row_stride, 0, k_out ? k_out_row_stride : 0, n_kv_heads,
+                 k == k_out && !k_weight && !pool};
+  }
+  if (pool) {
+    p.k_pool = NrPool{pool->k, pool->k_page_stride, pool->k_row_stride, pool->k_head_stride};
+    if (v) p.v_pool = NrPool{pool->v, pool->v_page_stride, pool->v_row_stride, pool->v_head_stride};
+    p.page_shift = log2_of(pool->page_size);
+    p.n_slots = (int64_t)pool->num_pages * pool->page_size;
+    p.slots = slots;
+  }
+  p.v = v;
+  p.v_stride = v_row_stride;
+  p.d_v = v ? d_v : 0;
+  // arguments that are not given are null or zero here and constrain nothing
+  const int vec = nr_vec(p.s, size,
+                         {p.q.x, p.q.out, p.q.w, p.k.x, p.k.out, p.k.w, p.k_pool.base, p.v_pool.base, p.v},
+                         {p.q.x_stride, p.q.out_stride, p.k.x_stride, p.k.out_stride, p.k_pool.page_stride,
+                          p.k_pool.row_stride, p.k_pool.head_stride, p.v_pool.page_stride, p.v_pool.row_stride,
+                          p.v_pool.head_stride, v ? p.v_stride : 0, p.d_v});
+  const int nv = nr_tasks(&p.s, vec);
+  const int rows = 32 / p.s.lph;
+  const int64_t groups = (n_heads + rows - 1) / rows + (n_kv_heads + rows - 1) / rows +
+                         (v ? ((int64_t)n_kv_heads * d_v / vec + 31) / 32 : 0);
+  p.parts = nr_parts(tokens, groups);
+  if (!nr_fwd(p, dtype, vec, nv, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return LOZA_OK;
+}
+
+size_t loza_qk_norm_rope_workspace_size(int32_t norm_dim) {
+  if (norm_dim < 1 || norm_dim > 1024) return 0;
+  return (size_t)nr_bwd_max_ctas() * norm_dim * sizeof(float);
+}
+
+loza_status loza_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                       const int32_t* positions, const double* inv_freq, int64_t tokens,
+                                       int32_t n_heads, int32_t n_kv_heads, int32_t d, int64_t dq_out_row_stride,
+                                       int64_t dk_out_row_stride, int64_t q_row_stride, int64_t k_row_stride,
+                                       const void* q_weight, const void* k_weight, int32_t norm_dim, float eps,
+                                       loza_rope_params rope, int32_t dtype, void* dq, int64_t dq_row_stride,
+                                       void* dk, int64_t dk_row_stride, float* dq_weight, float* dk_weight,
+                                       void* workspace, size_t workspace_bytes, loza_stream_t stream) {
+  NrBwdParams p{};
+  const loza_status rc = nr_shape(&p.s, tokens, d, norm_dim, eps, positions, inv_freq, rope, dtype);
+  if (rc != LOZA_OK) return rc;
+  if (n_heads < 0 || n_kv_heads < 0 || n_heads > 65535 || n_kv_heads > 65535 || n_heads + n_kv_heads < 1)
+    return LOZA_ERR_INVALID_ARG;
+  const int size = elt_size(dtype);
+  if ((q_weight || k_weight) && norm_dim < 1) return LOZA_ERR_INVALID_ARG;
+  if ((q_weight && n_heads < 1) || (k_weight && n_kv_heads < 1)) return LOZA_ERR_INVALID_ARG;
+  if (!aligned_to(q_weight, size) || !aligned_to(k_weight, size)) return LOZA_ERR_INVALID_ARG;
+  if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr))
+    return LOZA_ERR_INVALID_ARG;
+  if (!aligned_to(dq_weight, 4) || !aligned_to(dk_weight, 4)) return LOZA_ERR_INVALID_ARG;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (tokens == 0) {  // the weights' gradients are sums over nothing
+    if (dq_weight && cudaMemsetAsync(dq_weight, 0, (size_t)norm_dim * 4, st) != cudaSuccess) return LOZA_ERR_CUDA;
+    if (dk_weight && cudaMemsetAsync(dk_weight, 0, (size_t)norm_dim * 4, st) != cudaSuccess) return LOZA_ERR_CUDA;
+    return LOZA_OK;
+  }
+  if (n_heads > 0 && (!nr_rows_ok(dq_out, dq_out_row_stride, n_heads, d, size) ||
+                      !nr_rows_ok(dq, dq_row_stride, n_heads, d, size) ||
+                      (q_weight && !nr_rows_ok(q, q_row_stride, n_heads, d, size))))
+    return LOZA_ERR_INVALID_ARG;
+  if (n_kv_heads > 0 && (!nr_rows_ok(dk_out, dk_out_row_stride, n_kv_heads, d, size) ||
+                         !nr_rows_ok(dk, dk_row_stride, n_kv_heads, d, size) ||
+                         (k_weight && !nr_rows_ok(k, k_row_stride, n_kv_heads, d, size))))
+    return LOZA_ERR_INVALID_ARG;
+  // a gradient may replace its own input (the same rows), nothing else
+  if ((n_heads > 0 && ((dq == dq_out && dq_row_stride != dq_out_row_stride) ||
+                       (q_weight && dq == q && dq_row_stride != q_row_stride))) ||
+      (n_kv_heads > 0 && ((dk == dk_out && dk_row_stride != dk_out_row_stride) ||
+                          (k_weight && dk == k && dk_row_stride != k_row_stride))))
+    return LOZA_ERR_INVALID_ARG;
+  const bool sums = q_weight || k_weight;
+  if (sums) {
+    if (!workspace || !aligned16(workspace)) return LOZA_ERR_INVALID_ARG;
+    if (workspace_bytes < loza_qk_norm_rope_workspace_size(norm_dim)) return LOZA_ERR_WORKSPACE;
+  }
+  p.s.sign = -1.f;
+  if (n_heads > 0)
+    p.q = NrSide{q_weight ? q : nullptr, dq_out, q_weight, dq, q_weight ? q_row_stride : 0, dq_out_row_stride,
+                 dq_row_stride, n_heads, 0};
+  if (n_kv_heads > 0)
+    p.k = NrSide{k_weight ? k : nullptr, dk_out, k_weight, dk, k_weight ? k_row_stride : 0, dk_out_row_stride,
+                 dk_row_stride, n_kv_heads, 0};
+  p.partial = static_cast<float*>(workspace);
+  const int vec = nr_vec(p.s, size, {p.q.x, p.q.dy, p.q.w, p.q.out, p.k.x, p.k.dy, p.k.w, p.k.out},
+                         {p.q.x_stride, p.q.dy_stride, p.q.out_stride, p.k.x_stride, p.k.dy_stride, p.k.out_stride});
+  const int nv = nr_tasks(&p.s, vec);
+  const int rows = 32 / p.s.lph;
+  const int64_t gq = (n_heads + rows - 1) / rows, gk = (n_kv_heads + rows - 1) / rows;
+  // CTAs in proportion to the rows; at least one per side that has any
+  const int64_t most = std::min<int64_t>(nr_bwd_max_ctas(), (tokens * (gq + gk) + kNrWarps - 1) / kNrWarps + 1);
+  int64_t cq = (most * n_heads + (n_heads + n_kv_heads) / 2) / (n_heads + n_kv_heads);
+  if (n_heads > 0 && n_kv_heads > 0) cq = std::max<int64_t>(1, std::min<int64_t>(cq, most - 1));
+  p.q_ctas = (int)cq;
+  const int64_t ck = most - cq;
+  auto parts = [&](int64_t ctas, int64_t groups) {
+    if (ctas < 1 || groups < 1) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(groups, (ctas * kNrWarps + tokens - 1) / tokens));
+  };
+  p.parts_q = parts(cq, gq);
+  p.parts_k = parts(ck, gk);
+  if (!nr_bwd(p, dtype, vec, nv, (int)most, st)) return LOZA_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  if (sums) {
+    const NrDwParams dw{p.partial, dq_weight, dk_weight, norm_dim, p.q_ctas, (int)most};
+    if (!launch_after(norm_rope_dw_kernel, dim3((norm_dim + 31) / 32, 2), 256, st, dw)) return LOZA_ERR_CUDA;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+  }
+  return LOZA_OK;
+}
+
+size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, int32_t d_qk, int32_t d_v) {
+  if (!pkv_shape_ok(n_heads, n_kv_heads, d_qk, d_v)) return 0;
+  return pkv_workspace_bytes(d_v);
+}
+
+loza_status loza_ssa_decode_paged_kv(const void* q, int64_t q_row_stride, const loza_kv_pool* pool,
+                                     const int32_t* block_table, int64_t bt_stride, const int32_t* seqlens,
+                                     int32_t batch, int32_t max_seqlen, int32_t n_heads, int32_t n_kv_heads,
+                                     int32_t d_qk, int32_t d_v, loza_ssa_params params, int32_t dtype, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, loza_stream_t stream) {
+  if (!q || !pool || !pool->k || !pool->v || !block_table || !seqlens || !out || !lse) return LOZA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(pool->k) || !aligned16(pool->v) || !aligned16(out)) return LOZA_ERR_INVALID_ARG;
+  if (batch < 1 || batch > 65535 || max_seqlen < 1) return LOZA_ERR_INVALID_ARG;
+  if (!pool_page_ok(*pool)) return LOZA_ERR_INVALID_ARG;
+  if (!pool_strides_ok(pool->k_page_stride, pool->k_row_stride, pool->k_head_stride) ||
+      !pool_strides_ok(pool->v_page_stride, pool->v_row_stride, pool->v_head_stride))
+    return LOZA_ERR_INVALID_ARG;
+  for (int64_t s : {pool->k_page_stride, pool->k_row_stride, pool->k_head_stride, pool->v_page_stride,
+                    pool->v_row_stride, pool->v_head_stride, q_row_stride})
+    if (s % 8 != 0) return LOZA_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 || n_heads > 65535) return LOZA_ERR_INVALID_ARG;
+  if (q_row_stride < (int64_t)n_heads * d_qk || q_row_stride >= (int64_t(1) << 40)) return LOZA_ERR_INVALID_ARG;
+  if (bt_stride < ((int64_t)max_seqlen + pool->page_size - 1) / pool->page_size) return LOZA_ERR_INVALID_ARG;
+  if (dtype != LOZA_BF16 && dtype != LOZA_FP16 && dtype != LOZA_FP32) return LOZA_ERR_INVALID_ARG;
+  if (!window_ok(params) || dtype == LOZA_FP32 || pool->page_size < 16 ||
+      !pkv_shape_ok(n_heads, n_kv_heads, d_qk, d_v))
+    return LOZA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace)) return LOZA_ERR_INVALID_ARG;
+  if (workspace_bytes < pkv_workspace_bytes(d_v)) return LOZA_ERR_WORKSPACE;
+  PagedKvParams p{};
+  p.q = q;
+  p.q_stride = q_row_stride;
+  p.k = pool->k;
+  p.v = pool->v;
+  p.k_page = pool->k_page_stride;
+  p.k_row = pool->k_row_stride;
+  p.k_head = pool->k_head_stride;
+  p.v_page = pool->v_page_stride;
+  p.v_row = pool->v_row_stride;
+  p.v_head = pool->v_head_stride;
+  p.table = block_table;
+  p.table_stride = bt_stride;
+  p.seqlens = seqlens;
+  p.batch = batch;
+  p.max_seqlen = max_seqlen;
+  p.num_pages = pool->num_pages;
+  p.page_shift = log2_of(pool->page_size);
+  p.n_kv = n_kv_heads;
+  p.group = n_heads / n_kv_heads;
+  p.chunks = (p.group + kPkvHeads - 1) / kPkvHeads;
+  p.chunk = (p.group + p.chunks - 1) / p.chunks;
+  p.win = host_window(params);
+  p.scale_log2 = params.scale * 1.4426950408889634f;
+  p.out = out;
+  p.lse = lse;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pkv_part_o_bytes(d_v));
+  p.ctas = pkv_ctas();
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == LOZA_BF16 ? pkv_dispatch<__nv_bfloat16>(p, d_qk, st) : pkv_dispatch<__half>(p, d_qk, st);
+}
+
+}  // extern "C"

@@ -426,6 +426,212 @@ loza_status loza_ssa_merge(const void *o_a, const float *lse_a, const void *o_b,
 loza_status loza_ssa_mix(const void *o_full, const void *o_ssa, int64_t n, float alpha, void *out,
                          loza_stream_t stream);
 
+/*
+ * Serving and training around the attention: the bookkeeping of a paged
+ * cache, the position rotation, norms of query and key heads, and decode over
+ * paged K and V pools. (The LoZA pages name rotary dimensions (the 64 of 192
+ * and 576) and paged caches only as part of the models the attention runs in;
+ * these entry points are for the callers of this library.)
+ */
+
+/* Element types of these entry points (the other ones are bf16). */
+#define LOZA_BF16 0
+#define LOZA_FP16 1
+#define LOZA_FP32 2
+
+/*
+ * A paged cache: two pools of num_pages pages of page_size rows (a power of
+ * two up to 65,536; num_pages * page_size <= INT32_MAX). Head h of row r of page
+ * g is at base + g * page_stride + r * row_stride + h * head_stride elements,
+ * its columns contiguous; so [pages, rows, heads, d] and [pages, heads, rows,
+ * d] arrays, and K and V side by side in one array, are all pools. Strides are
+ * in elements and >= 0. A row's number in the pool (its slot) is g *
+ * page_size + r.
+ */
+typedef struct {
+    void *k;
+    void *v;               /* NULL: the latent cache, whose values are columns of k */
+    int32_t num_pages;
+    int32_t page_size;
+    int64_t k_page_stride, k_row_stride, k_head_stride;
+    int64_t v_page_stride, v_row_stride, v_head_stride;
+} loza_kv_pool;
+
+/*
+ * Which columns of a head are rotated, and how: rope_dim columns (even; 0: no
+ * rotation) from rope_offset. Pair i of them is (i, i + rope_dim / 2) or, if
+ * interleaved is 1, (2i, 2i + 1). Pair i of a token at position t turns by t *
+ * inv_freq[i]; cos and sin are multiplied by scale (1 unless the frequencies
+ * were stretched by a method that asks for it).
+ */
+typedef struct {
+    int32_t rope_dim;
+    int32_t rope_offset;
+    int32_t interleaved;
+    float scale;
+} loza_rope_params;
+
+/* How loza_rope_frequencies stretches the frequencies for long contexts. */
+#define LOZA_ROPE_NONE 0
+#define LOZA_ROPE_LINEAR 1   /* every frequency divided by factor */
+#define LOZA_ROPE_NTK 2      /* theta * factor ^ (rope_dim / (rope_dim - 2)) */
+#define LOZA_ROPE_YARN 3     /* frequencies that make fewer than beta_slow turns over original_max
+                                positions are divided by factor, those with more than beta_fast
+                                turns kept, a linear ramp over the pair index between; scale
+                                0.1 ln(factor) + 1 */
+
+/*
+ * The step's bookkeeping of a paged cache. Request r has ctx_lens[r] tokens in
+ * the cache, in pages block_table[r * bt_stride + 0 ...], and appends
+ * new_lens[r] tokens (0: it is idle in this step). Pages that the new tokens
+ * need are taken from free_pages[0 .. n_free) in request order and entered in
+ * the table after the ones it holds; entries before them and behind them are
+ * left as they were. Written:
+ *   cu_seqlens [batch + 1]  offsets of the requests' new tokens in the packed rows
+ *   seqlens    [batch]      ctx + new, the cached lengths after the step
+ *   positions, slots [capacity]  position and pool row of each packed token;
+ *                           rows past the last token get position 0, slot -1
+ *                           (which loza_qk_norm_rope does not write), so a
+ *                           captured step can run at a fixed capacity
+ *   counts     [3]          new tokens, pages taken, requests that were short
+ * A request is short if its pages would not fit the table's max_pages columns
+ * or reach past n_free: it gets no page, its new tokens slot -1 and its
+ * seqlens stays ctx. Pages are dealt as if nobody were short, so pages taken
+ * can exceed n_free; the caller that sees counts[2] > 0 frees pages and calls
+ * again (the same call with the same lengths gives the same result). Tokens
+ * past capacity are counted but not written. A negative page number in the
+ * part of the table that a request holds (a page handed back because the
+ * window left it) gives slot -1. Lengths outside [0, 2^30) count as 0.
+ * All pointers are device memory; positions and slots 16-byte aligned; page
+ * numbers in free_pages must be distinct and not in use. max_pages <=
+ * bt_stride; page_size a power of two up to 65,536; at most 16,384 requests
+ * (LOZA_ERR_UNSUPPORTED beyond).
+ */
+loza_status loza_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, int32_t batch,
+                           const int32_t *free_pages, int32_t n_free, int32_t page_size,
+                           int32_t *block_table, int64_t bt_stride, int32_t max_pages, int64_t capacity,
+                           int32_t *cu_seqlens, int32_t *seqlens, int32_t *positions, int64_t *slots,
+                           int32_t *counts, loza_stream_t stream);
+
+/*
+ * Host function: the angles per position of rope_dim / 2 pairs,
+ * theta^(-2i / rope_dim) stretched by `scaling`, into inv_freq (HOST memory,
+ * rope_dim / 2 doubles), and the factor for loza_rope_params.scale. factor >= 1
+ * is the ratio of the extended to the original context length; original_max,
+ * beta_fast and beta_slow are read by LOZA_ROPE_YARN only (usually 32 and 1).
+ * Angles are 64-bit throughout: a 32-bit product is off by 0.03 rad at
+ * position 10^6. Any other table of frequencies may be used as well.
+ */
+loza_status loza_rope_frequencies(double theta, int32_t rope_dim, int32_t scaling, double factor,
+                                  double original_max, double beta_fast, double beta_slow,
+                                  double *inv_freq, float *scale);
+
+/*
+ * Rotation of one tensor: out[t, h] = x[t, h] with the columns of `rope` turned
+ * by positions[t]. x, out [tokens, n_heads, d] (d <= 1024), rows x_row_stride
+ * and out_row_stride elements apart, heads contiguous within a row, dtype any
+ * of the three; positions device int32 [tokens] (any value); inv_freq DEVICE
+ * double [rope_dim / 2]. out may be x with the same stride (then only the
+ * rotated columns are touched) or must not overlap it. transposed = 1 applies
+ * the transposed map, which is the gradient: dx from dout. 32-bit arithmetic,
+ * one rounding. Sizes, offsets, strides and pointers that are multiples of 16
+ * bytes run in 16-byte vectors; others, element by element.
+ */
+loza_status loza_rope(const void *x, const int32_t *positions, const double *inv_freq, int64_t tokens,
+                      int32_t n_heads, int32_t d, int64_t x_row_stride, loza_rope_params rope,
+                      int32_t transposed, int32_t dtype, void *out, int64_t out_row_stride,
+                      loza_stream_t stream);
+
+/*
+ * Norm of each query and key head, the rotation, and the write into a paged
+ * cache, in one pass. Per head row x of q [tokens, n_heads, d] and k [tokens,
+ * n_kv_heads, d]:
+ *     n_c = weight_c x_c / sqrt(mean(x_0 .. x_{norm_dim-1} squared) + eps)  for c < norm_dim
+ *     n_c = x_c  for the other columns, and for a side whose weight is NULL
+ * then the rotation of loza_rope; 32-bit arithmetic, one rounding.
+ *   q, k, v   rows q_row_stride, k_row_stride, v_row_stride elements apart, so
+ *             they may be slices of one projection's rows; n_heads or
+ *             n_kv_heads may be 0 (that side's arguments are then not read)
+ *   q_weight, k_weight  [norm_dim] of the same dtype, or NULL
+ *   q_out, k_out  as q and k, with their own row strides; each may be its
+ *             input with the same stride, or must not overlap any input.
+ *             k_out may be NULL when a pool is given
+ *   pool      NULL, or the cache: token t's key heads (after norm and
+ *             rotation) and v's rows [n_kv_heads, d_v] go to row slots[t];
+ *             a slot outside [0, num_pages * page_size) writes nothing.
+ *             pool->v and v are both given or both NULL (the latent cache:
+ *             d = 576, norm_dim = 512, rope_offset = 512). Slots must be
+ *             distinct (except those that write nothing); every page_size
+ *             from 1 on is taken here
+ *   slots     device int64 [tokens] (from loza_page_plan), NULL without a pool
+ */
+loza_status loza_qk_norm_rope(const void *q, const void *k, const void *v, const int32_t *positions,
+                              const double *inv_freq, int64_t tokens, int32_t n_heads, int32_t n_kv_heads,
+                              int32_t d, int32_t d_v, int64_t q_row_stride, int64_t k_row_stride,
+                              int64_t v_row_stride, const void *q_weight, const void *k_weight,
+                              int32_t norm_dim, float eps, loza_rope_params rope, int32_t dtype,
+                              void *q_out, int64_t q_out_row_stride, void *k_out, int64_t k_out_row_stride,
+                              const loza_kv_pool *pool, const int64_t *slots, loza_stream_t stream);
+
+/* Bytes of workspace loza_qk_norm_rope_backward needs when a weight is given (0: norm_dim out of range). */
+size_t loza_qk_norm_rope_workspace_size(int32_t norm_dim);
+
+/*
+ * Gradient of loza_qk_norm_rope: from dq_out and dk_out (the gradients of
+ * q_out and k_out) and the forward's inputs, dq, dk (same dtype) and the
+ * weights' gradients dq_weight, dk_weight ([norm_dim] fp32, written, summed
+ * over all tokens and heads; each given exactly if its weight is). A side
+ * without weight needs no q (k). The sums' order is fixed: no atomics, the
+ * same bits every run on one kind of GPU. dq may replace dq_out or q, and dk
+ * dk_out or k, with the same row strides.
+ *   workspace: loza_qk_norm_rope_workspace_size(norm_dim) bytes, 16-byte
+ *   aligned, unless both weights are NULL; contents on entry are ignored
+ */
+loza_status loza_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                                       const int32_t *positions, const double *inv_freq, int64_t tokens,
+                                       int32_t n_heads, int32_t n_kv_heads, int32_t d,
+                                       int64_t dq_out_row_stride, int64_t dk_out_row_stride,
+                                       int64_t q_row_stride, int64_t k_row_stride, const void *q_weight,
+                                       const void *k_weight, int32_t norm_dim, float eps,
+                                       loza_rope_params rope, int32_t dtype, void *dq, int64_t dq_row_stride,
+                                       void *dk, int64_t dk_row_stride, float *dq_weight, float *dk_weight,
+                                       void *workspace, size_t workspace_bytes, loza_stream_t stream);
+
+/* Bytes of workspace loza_ssa_decode_paged_kv needs, whatever the batch and the lengths (0: unsupported shape). */
+size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, int32_t d_qk, int32_t d_v);
+
+/*
+ * Decode over paged K and V pools with heads of their own or shared by groups:
+ * the operation of loza_ssa_decode (window `p` at the sequence's last position,
+ * LOZA_UNBOUNDED included) for n_heads a multiple of n_kv_heads, (d_qk, d_v) in
+ * {(64,64), (128,128), (192,128)}, bf16 or fp16. The work is split over the
+ * keys of all sequences together, so one long sequence and many ragged ones
+ * both fill the GPU.
+ *   q       [batch, n_heads, d_qk], rows q_row_stride elements apart
+ *   pool    both pools given, 16-byte aligned, every stride a multiple of 8
+ *           elements, page_size >= 16
+ *   block_table  device int32, page of key t of sequence n: block_table[n *
+ *           bt_stride + t / page_size]; bt_stride >= ceil(max_seqlen /
+ *           page_size). Only entries of pages that hold a key below
+ *           seqlens[n] within 64 keys of the window are read. A page number
+ *           outside [0, num_pages) holds no keys: they get no weight
+ *   seqlens device int32 [batch], 0 <= seqlens[n] <= max_seqlen (taken to be
+ *           in that range if it is not); the query of sequence n is its key
+ *           seqlens[n] - 1. A sequence of length 0 (an idle row of a padded
+ *           batch), or none of whose pages is there, gives out 0 and lse -inf
+ *   Rows at or past seqlens[n], and rows outside the window, are not read.
+ *   out     [batch, n_heads, d_v] of the same dtype; lse [batch, n_heads] fp32
+ *   workspace  loza_decode_paged_kv_workspace_size(...) bytes, 16-byte
+ *           aligned, contents on entry ignored; calls that can overlap on the
+ *           GPU need one each
+ */
+loza_status loza_ssa_decode_paged_kv(const void *q, int64_t q_row_stride, const loza_kv_pool *pool,
+                                     const int32_t *block_table, int64_t bt_stride, const int32_t *seqlens,
+                                     int32_t batch, int32_t max_seqlen, int32_t n_heads, int32_t n_kv_heads,
+                                     int32_t d_qk, int32_t d_v, loza_ssa_params p, int32_t dtype,
+                                     void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                     loza_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char *loza_status_string(loza_status s);
 
