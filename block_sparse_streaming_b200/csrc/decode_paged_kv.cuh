@@ -32,6 +32,7 @@
 
 #include <cuda_fp16.h>
 
+#include "norm_rope.cuh"
 #include "prefill.cuh"
 #include "sm100.cuh"
 
@@ -127,14 +128,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// 16 bytes global -> shared; `bytes` 0 fills with zeros and reads nothing.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 template <int DQK, int DV>
 struct PagedKvLayout {
   static constexpr int kTileBytes = 16 * (DQK + DV) * 2;  // one warp's K and V rows of a step

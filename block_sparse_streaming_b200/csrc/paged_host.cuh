@@ -11,6 +11,13 @@ namespace {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Of a power of two.
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
 // A kernel behind the one that writes what it reads (it waits for it itself).
 template <typename P>
 bool launch_after(void (*kernel)(P), dim3 grid, unsigned threads, cudaStream_t st, const P& prm) {
@@ -48,7 +55,7 @@ loza_status nr_shape(NrShape* s, int64_t tokens, int32_t d, int32_t norm_dim, fl
   s->d = d;
   s->norm_dim = norm_dim;
   s->rope_off = r.rope_offset;
-  s->half = r.rope_dim / 2;
+  s->pairs = r.rope_dim / 2;
   s->interleaved = r.interleaved;
   s->scale = r.scale;
   s->sign = 1.f;
@@ -67,7 +74,7 @@ bool nr_rows_ok(const void* x, int64_t stride, int heads, int d, int size) {
 // Largest vector (in elements) that every size, offset and stride allows: 16 bytes, or one element.
 int nr_vec(const NrShape& s, int size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> sizes) {
   const int v = 16 / size;
-  if (s.d % v || s.norm_dim % v || s.rope_off % v || s.half % v) return 1;
+  if (s.d % v || s.norm_dim % v || s.rope_off % v || s.pairs % v) return 1;
   for (const void* p : ptrs)
     if (!aligned16(p)) return 1;
   for (int64_t n : sizes)
@@ -77,8 +84,8 @@ int nr_vec(const NrShape& s, int size, std::initializer_list<const void*> ptrs, 
 
 // Tasks (pairs of vectors) of a row, and how many a lane takes; returns that number (NV).
 int nr_tasks(NrShape* s, int vec) {
-  s->nrope = s->half / vec;
-  s->npass = (s->d - 2 * s->half) / vec;
+  s->nrope = s->pairs / vec;
+  s->npass = (s->d - 2 * s->pairs) / vec;
   s->ntasks = s->nrope + (s->npass + 1) / 2;
   int nv = vec == 1 ? 4 : 1;
   while (nv * 32 < s->ntasks) nv = vec == 1 ? 16 : nv * 2;
@@ -87,66 +94,101 @@ int nr_tasks(NrShape* s, int vec) {
   return nv;
 }
 
-template <typename T, int VEC, int NV>
+// Angles of a batch, at most: eight tokens of the longest table (512 pairs) fit, so a warp always has its token.
+constexpr int64_t kNrTableBytes = kNrWarps * 512 * sizeof(float2);
+
+template <typename T, int VEC, int NV, bool NORM, bool INTER>
 bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
-  const int64_t grid = (p.s.tokens * p.parts + kNrWarps - 1) / kNrWarps;
-  const size_t smem = (size_t)kNrWarps * p.s.half * sizeof(float2);
-  norm_rope_kernel<T, VEC, NV><<<(unsigned)grid, kNrThreads, smem, st>>>(p);
+  auto kernel = norm_rope_kernel<T, VEC, NV, NORM, INTER>;
+  const size_t smem = NrRing<VEC, NV, 1>::kBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  kernel<<<(unsigned)(p.ctas * p.parts), kNrThreads, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess;
 }
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, bool INTER>
 bool nr_launch_bwd(const NrBwdParams& p, int ctas, cudaStream_t st) {
-  const size_t smem = (size_t)kNrWarps * (p.s.half * sizeof(float2) + p.s.norm_dim * sizeof(float));
-  norm_rope_backward_kernel<T, VEC, NV><<<(unsigned)ctas, kNrThreads, smem, st>>>(p);
+  auto kernel = norm_rope_backward_kernel<T, VEC, NV, INTER>;
+  const size_t smem = NrRing<VEC, NV, 2>::kBytes +
+                      std::max((size_t)2 * std::max(p.batch_q, p.batch_k) * p.s.pairs * sizeof(float2),
+                               (size_t)kNrWarps * p.s.norm_dim * sizeof(float));
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  kernel<<<(unsigned)ctas, kNrThreads, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess;
 }
 
-template <typename T>
-bool nr_fwd16(const NrFwdParams& p, int vec, int nv, cudaStream_t st) {
-  if (vec == 8) return nv == 1 ? nr_launch_fwd<T, 8, 1>(p, st) : nr_launch_fwd<T, 8, 2>(p, st);
-  return nv == 4 ? nr_launch_fwd<T, 1, 4>(p, st) : nr_launch_fwd<T, 1, 16>(p, st);
+// One element per vector: both layouts are one kernel, and the rotation alone is the kernel of the norm.
+template <typename T, int VEC, int NV>
+bool nr_launch(const NrFwdParams& p, int, cudaStream_t st) {
+  const bool norm = p.q.w || p.k.w;
+  if constexpr (VEC == 1) return nr_launch_fwd<T, VEC, NV, true, false>(p, st);
+  else if (p.s.interleaved)
+    return norm ? nr_launch_fwd<T, VEC, NV, true, true>(p, st) : nr_launch_fwd<T, VEC, NV, false, true>(p, st);
+  else
+    return norm ? nr_launch_fwd<T, VEC, NV, true, false>(p, st) : nr_launch_fwd<T, VEC, NV, false, false>(p, st);
 }
-bool nr_fwd32(const NrFwdParams& p, int vec, int nv, cudaStream_t st) {
-  if (vec == 4)
-    return nv == 1   ? nr_launch_fwd<float, 4, 1>(p, st)
-           : nv == 2 ? nr_launch_fwd<float, 4, 2>(p, st)
-                     : nr_launch_fwd<float, 4, 4>(p, st);
-  return nv == 4 ? nr_launch_fwd<float, 1, 4>(p, st) : nr_launch_fwd<float, 1, 16>(p, st);
-}
-bool nr_fwd(const NrFwdParams& p, int dtype, int vec, int nv, cudaStream_t st) {
-  if (dtype == LOZA_BF16) return nr_fwd16<__nv_bfloat16>(p, vec, nv, st);
-  if (dtype == LOZA_FP16) return nr_fwd16<__half>(p, vec, nv, st);
-  return nr_fwd32(p, vec, nv, st);
-}
-
-template <typename T>
-bool nr_bwd16(const NrBwdParams& p, int vec, int nv, int ctas, cudaStream_t st) {
-  if (vec == 8) return nv == 1 ? nr_launch_bwd<T, 8, 1>(p, ctas, st) : nr_launch_bwd<T, 8, 2>(p, ctas, st);
-  return nv == 4 ? nr_launch_bwd<T, 1, 4>(p, ctas, st) : nr_launch_bwd<T, 1, 16>(p, ctas, st);
-}
-bool nr_bwd32(const NrBwdParams& p, int vec, int nv, int ctas, cudaStream_t st) {
-  if (vec == 4)
-    return nv == 1   ? nr_launch_bwd<float, 4, 1>(p, ctas, st)
-           : nv == 2 ? nr_launch_bwd<float, 4, 2>(p, ctas, st)
-                     : nr_launch_bwd<float, 4, 4>(p, ctas, st);
-  return nv == 4 ? nr_launch_bwd<float, 1, 4>(p, ctas, st) : nr_launch_bwd<float, 1, 16>(p, ctas, st);
-}
-bool nr_bwd(const NrBwdParams& p, int dtype, int vec, int nv, int ctas, cudaStream_t st) {
-  if (dtype == LOZA_BF16) return nr_bwd16<__nv_bfloat16>(p, vec, nv, ctas, st);
-  if (dtype == LOZA_FP16) return nr_bwd16<__half>(p, vec, nv, ctas, st);
-  return nr_bwd32(p, vec, nv, ctas, st);
+template <typename T, int VEC, int NV>
+bool nr_launch(const NrBwdParams& p, int ctas, cudaStream_t st) {
+  if constexpr (VEC == 1) return nr_launch_bwd<T, VEC, NV, false>(p, ctas, st);
+  else
+    return p.s.interleaved ? nr_launch_bwd<T, VEC, NV, true>(p, ctas, st)
+                           : nr_launch_bwd<T, VEC, NV, false>(p, ctas, st);
 }
 
-// Warps per token of the forward: enough to give every SM 16 warps while
-// there are few tokens, never more than a token has row groups.
-int nr_parts(int64_t tokens, int64_t groups) {
-  const int64_t want = ((int64_t)sm_count() * 16 + tokens - 1) / tokens;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, groups, 64}));
+// The instance for a type, vector length and tasks per lane (see nr_vec and nr_tasks).
+template <typename Params>
+bool nr_run(const Params& p, int dtype, int vec, int nv, int ctas, cudaStream_t st) {
+  if (dtype == LOZA_FP32) {
+    if (vec == 4)
+      return nv == 1   ? nr_launch<float, 4, 1>(p, ctas, st)
+             : nv == 2 ? nr_launch<float, 4, 2>(p, ctas, st)
+                       : nr_launch<float, 4, 4>(p, ctas, st);
+    return nv == 4 ? nr_launch<float, 1, 4>(p, ctas, st) : nr_launch<float, 1, 16>(p, ctas, st);
+  }
+  auto half = [&](auto zero) {
+    using T = decltype(zero);
+    if (vec == 8) return nv == 1 ? nr_launch<T, 8, 1>(p, ctas, st) : nr_launch<T, 8, 2>(p, ctas, st);
+    return nv == 4 ? nr_launch<T, 1, 4>(p, ctas, st) : nr_launch<T, 1, 16>(p, ctas, st);
+  };
+  return dtype == LOZA_BF16 ? half(__nv_bfloat16()) : half(__half());
 }
 
-constexpr int kNrBwdCtasPerSm = 4;
-int nr_bwd_max_ctas() { return sm_count() * kNrBwdCtasPerSm; }
+// CTAs that fill the GPU: two per SM (launch bounds), one of the wide rows' instances.
+int nr_ctas(int vec, int nv) { return sm_count() * (nv * vec > 8 ? 1 : 2); }
+
+// Log2 of the warps that share a token: one warp takes whole tokens unless
+// that leaves some of `warps` without work; at most `most` of them, and never
+// more than the widest side has groups.
+int nr_wide(int64_t tokens, int64_t groups, int64_t warps, int64_t most) {
+  int w = 0;
+  while ((int64_t(2) << w) <= std::min(groups, most) && (tokens << w) < warps) ++w;
+  return w;
+}
+
+// Tokens per step of a CTA: `each` per warp (or group of warps), as far as the angles fit.
+int nr_batch(const NrShape& s, int wide_log, int64_t each) {
+  const int64_t step = std::max(1, kNrWarps >> wide_log);
+  int64_t b = step * each;
+  if (s.pairs > 0) b = std::min<int64_t>(b, kNrTableBytes / ((int64_t)s.pairs * sizeof(float2)));
+  return (int)(b / step * step);
+}
+
+// The forward's walk, from the groups of the widest side. With fewer tokens
+// than CTAs several CTAs share a token.
+void nr_plan_fwd(NrFwdParams* p, int vec, int nv, int64_t groups) {
+  const int64_t ctas = nr_ctas(vec, nv);
+  p->wide_log = nr_wide(p->s.tokens, groups, ctas * kNrWarps, 64);
+  p->parts = std::max(1, (1 << p->wide_log) / kNrWarps);
+  p->ctas = (int)std::min<int64_t>(p->s.tokens, ctas);
+  p->batch = nr_batch(p->s, p->wide_log, 1);
+}
+
+// CTAs of the backward at most (the workspace holds a row of sums per side for each).
+int nr_bwd_max_ctas() { return sm_count() * 2; }
 
 bool pool_page_ok(const loza_kv_pool& p) {
   return p.num_pages >= 1 && p.page_size >= 1 && p.page_size <= 65536 && (p.page_size & (p.page_size - 1)) == 0 &&
@@ -155,11 +197,6 @@ bool pool_page_ok(const loza_kv_pool& p) {
 bool pool_strides_ok(int64_t page, int64_t row, int64_t head) {
   const int64_t cap = int64_t(1) << 40;
   return page >= 0 && row >= 0 && head >= 0 && page < cap && row < cap && head < cap;
-}
-int log2_of(int v) {
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
 }
 
 // ---------------------------------------------------------------------------
@@ -311,8 +348,9 @@ loza_status loza_rope(const void* x, const int32_t* positions, const double* inv
     p.s.lph = 1;
     while (p.s.lph * nv < p.s.ntasks) p.s.lph *= 2;
   }
-  p.parts = nr_parts(tokens, (n_heads + 32 / p.s.lph - 1) / (32 / p.s.lph));
-  if (!nr_fwd(p, dtype, vec, nv, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
+  const int64_t groups = (n_heads + 32 / p.s.lph - 1) / (32 / p.s.lph);
+  nr_plan_fwd(&p, vec, nv, groups);
+  if (!nr_run(p, dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return LOZA_OK;
 }
@@ -381,17 +419,17 @@ loza_status loza_qk_norm_rope(const void* q, const void* k, const void* v, const
                           p.v_pool.head_stride, v ? p.v_stride : 0, p.d_v});
   const int nv = nr_tasks(&p.s, vec);
   const int rows = 32 / p.s.lph;
-  const int64_t groups = (n_heads + rows - 1) / rows + (n_kv_heads + rows - 1) / rows +
-                         (v ? ((int64_t)n_kv_heads * d_v / vec + 31) / 32 : 0);
-  p.parts = nr_parts(tokens, groups);
-  if (!nr_fwd(p, dtype, vec, nv, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
+  const int vper = p.d_v / vec;
+  p.vper_log = vper > 0 && (vper & (vper - 1)) == 0 ? log2_of(vper) : -1;
+  nr_plan_fwd(&p, vec, nv, (std::max(n_heads, n_kv_heads) + rows - 1) / rows);
+  if (!nr_run(p, dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return LOZA_OK;
 }
 
 size_t loza_qk_norm_rope_workspace_size(int32_t norm_dim) {
   if (norm_dim < 1 || norm_dim > 1024) return 0;
-  return (size_t)nr_bwd_max_ctas() * norm_dim * sizeof(float);
+  return (size_t)2 * nr_bwd_max_ctas() * norm_dim * sizeof(float);
 }
 
 loza_status loza_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
@@ -452,23 +490,19 @@ loza_status loza_qk_norm_rope_backward(const void* dq_out, const void* dk_out, c
   const int nv = nr_tasks(&p.s, vec);
   const int rows = 32 / p.s.lph;
   const int64_t gq = (n_heads + rows - 1) / rows, gk = (n_kv_heads + rows - 1) / rows;
-  // CTAs in proportion to the rows; at least one per side that has any
-  const int64_t most = std::min<int64_t>(nr_bwd_max_ctas(), (tokens * (gq + gk) + kNrWarps - 1) / kNrWarps + 1);
-  int64_t cq = (most * n_heads + (n_heads + n_kv_heads) / 2) / (n_heads + n_kv_heads);
-  if (n_heads > 0 && n_kv_heads > 0) cq = std::max<int64_t>(1, std::min<int64_t>(cq, most - 1));
-  p.q_ctas = (int)cq;
-  const int64_t ck = most - cq;
-  auto parts = [&](int64_t ctas, int64_t groups) {
-    if (ctas < 1 || groups < 1) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(groups, (ctas * kNrWarps + tokens - 1) / tokens));
+  const int64_t ctas = std::min<int64_t>(nr_ctas(vec, nv), tokens);
+  p.wide_log = nr_wide(tokens, std::max(gq, gk), ctas * kNrWarps, kNrWarps);
+  // a side of few groups is short: several tokens a warp between two barriers
+  auto each = [&](int64_t groups) {
+    return std::max<int64_t>(1, std::min<int64_t>(4, (int64_t(8) << p.wide_log) / std::max<int64_t>(1, groups)));
   };
-  p.parts_q = parts(cq, gq);
-  p.parts_k = parts(ck, gk);
-  if (!nr_bwd(p, dtype, vec, nv, (int)most, st)) return LOZA_ERR_CUDA;
+  p.batch_q = nr_batch(p.s, p.wide_log, each(gq));
+  p.batch_k = nr_batch(p.s, p.wide_log, each(gk));
+  if (!nr_run(p, dtype, vec, nv, (int)ctas, st)) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   if (sums) {
-    const NrDwParams dw{p.partial, dq_weight, dk_weight, norm_dim, p.q_ctas, (int)most};
-    if (!launch_after(norm_rope_dw_kernel, dim3((norm_dim + 31) / 32, 2), 256, st, dw)) return LOZA_ERR_CUDA;
+    const NrDwParams dw{p.partial, dq_weight, dk_weight, norm_dim, (int)ctas};
+    if (!launch_after(norm_rope_dw_kernel, dim3((norm_dim + 7) / 8, 2), 512, st, dw)) return LOZA_ERR_CUDA;
     g_launches.fetch_add(1, std::memory_order_relaxed);
   }
   return LOZA_OK;
