@@ -15,13 +15,15 @@
 // balance without the host knowing them. A CTA walks its range item by item.
 // An item that lies in one CTA is written out by it; the others leave
 // (reference, sum, weighted values) per range in the workspace, at most two
-// per CTA, which decode_paged_join_kernel adds up in the order of the CTAs.
+// per CTA, and the CTA where such an item begins leaves its place, by which
+// decode_paged_join_kernel adds the parts up in the order of the CTAs.
 // Nothing is atomic and the order of every sum is fixed by the lengths.
 //
 // Inside a CTA each of four warps owns 16 keys of every step and runs alone:
 // its own ring of tiles filled by 16-byte cp.async (masked rows and pages that
 // are not there are filled with zeros and never read from memory), its own
-// running maximum and sums; the four meet only at the end of an item. Keys are
+// running maximum and sums; the four meet only at the end of an item, while
+// the next item's queries and first tiles are on their way. Keys are
 // the rows of the matrix products, so a group of up to 8 heads (NT = 1) needs
 // no padding to 16: S^T (16 keys x 8 heads) = K Q^T, then O^T (d_v x 8 heads)
 // += V^T P^T, with P^T turned in registers by movmatrix. P is fed as two
@@ -58,6 +60,8 @@ struct PagedKvParams {
   void* out;                       // [batch, n_heads, d_v]
   float* lse;                      // [batch, n_heads]
   float *part_o, *part_ml;         // [ctas][2][16][d_v], [ctas][2][16][2]
+  int4* split;                     // [ctas]: {sequence, item, last CTA} of the item that begins in a CTA and ends in
+                                   // a later one; sequence -1: none
   int ctas;
 };
 
@@ -128,30 +132,44 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-template <int DQK, int DV>
+template <int DQK, int DV, int NT>
 struct PagedKvLayout {
   static constexpr int kTileBytes = 16 * (DQK + DV) * 2;  // one warp's K and V rows of a step
   static constexpr int kStages = DQK + DV <= 128 ? 6 : (DQK + DV <= 256 ? 3 : 2);
   static constexpr int kRing = kPkvWarps * kStages * kTileBytes;
-  static constexpr int kJoin = kPkvWarps * 8 * DV * 4;            // [warp][8 heads][d_v] fp32
+  static constexpr int kQBytes = 8 * NT * DQK * 2;                // each warp's copy of an item's queries
+  static constexpr int kQ = kPkvWarps * kQBytes;
   static constexpr int kMl = kPkvWarps * kPkvHeads * 2 * 4;       // [warp][16 heads]{reference, sum}
   static constexpr int kMask = kPkvWarps * kStages * 4;
-  static constexpr int kSmem = kRing + kJoin + kMl + kMask;
+  static constexpr int kSmem = kRing + kQ + kMl + kMask;
+  // a warp's weighted values of 8 heads go to its last stage, which a new item's first tiles leave free
+  static_assert(8 * DV * 4 <= kTileBytes, "the join's staging fits a stage");
+  static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
+};
+
+// A range of one item's steps: [step, s_end) of item `item` of sequence n.
+struct PagedKvPiece {
+  int n, item, step, s_end;
+  PagedKvSpan span;
 };
 
 template <typename T, int DQK, int DV, int NT>
 __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_kernel(const PagedKvParams p) {
-  using L = PagedKvLayout<DQK, DV>;
+  using L = PagedKvLayout<DQK, DV, NT>;
   constexpr int S = L::kStages;
   constexpr int KC = DQK / 8, VC = DV / 8;  // 16-byte chunks per row
   extern __shared__ __align__(128) uint8_t pkv_smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, c2 = (lane & 3) * 2;  // fragment row and first column of this lane
-  float* join = reinterpret_cast<float*>(pkv_smem + L::kRing);
-  float* ml = reinterpret_cast<float*>(pkv_smem + L::kRing + L::kJoin);
+  float* ml = reinterpret_cast<float*>(pkv_smem + L::kRing + L::kQ);
   volatile uint32_t* masks =
-      reinterpret_cast<volatile uint32_t*>(pkv_smem + L::kRing + L::kJoin + L::kMl) + warp * S;
+      reinterpret_cast<volatile uint32_t*>(pkv_smem + L::kRing + L::kQ + L::kMl) + warp * S;
   const uint32_t ring = smem_u32(pkv_smem) + (uint32_t)(warp * S * L::kTileBytes);
+  const uint32_t qbuf = smem_u32(pkv_smem) + (uint32_t)(L::kRing + warp * L::kQBytes);
+  // staging of warp w: in its last stage
+  auto staging = [&](int w) {
+    return reinterpret_cast<float*>(pkv_smem + (w * S + S - 1) * L::kTileBytes);
+  };
 
   // ---- this CTA's range of steps, found by every warp for itself
   const int items = p.n_kv * p.chunks;
@@ -165,7 +183,18 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
   total *= items;
   const int64_t ctas = min((int64_t)p.ctas, total);  // so that no range is empty
   griddep_launch_dependents();
-  if (blockIdx.x >= ctas) return;
+  // sequences without keys: their rows are nobody's item
+  for (int s = blockIdx.x; s < p.batch; s += gridDim.x) {
+    if (PagedKvSpan(p, s).steps > 0) continue;
+    const int64_t row = (int64_t)s * p.n_kv * p.group;
+    for (int x = tid; x < p.n_kv * p.group * VC; x += kPkvThreads)
+      reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * DV)[x] = make_uint4(0, 0, 0, 0);
+    for (int x = tid; x < p.n_kv * p.group; x += kPkvThreads) p.lse[row + x] = -INFINITY;
+  }
+  if (blockIdx.x >= ctas) {
+    if (tid == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
   const int64_t begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
   int n = 0;
   int64_t before = 0;  // steps of the sequences before n
@@ -186,10 +215,11 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
     }
     before += __shfl_sync(0xffffffffu, s, 31);
   }
-  PagedKvSpan span(p, n);
-  int item = (int)((begin - before) / span.steps);
-  int step = (int)((begin - before) % span.steps);
+  PagedKvPiece cur{n, 0, 0, 0, PagedKvSpan(p, n)};
+  cur.item = (int)((begin - before) / cur.span.steps);
+  cur.step = (int)((begin - before) % cur.span.steps);
   int64_t left = end - begin;
+  cur.s_end = (int)min((int64_t)cur.span.steps, cur.step + left);
 
   const T* kbase = static_cast<const T*>(p.k);
   const T* vbase = static_cast<const T*>(p.v);
@@ -232,37 +262,61 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
     }
     cp_async_commit();
   };
-  auto prologue = [&](const PagedKvSpan& sp, int seq, int kvh, int s, int s_end) {
+  // An item's queries into this warp's buffer (rows past the item's heads are zeros), and its first tiles.
+  auto prologue = [&](const PagedKvPiece& c, int first_page) {
     __syncwarp();  // every lane is past its reads of the ring
-    page_next = page_of(sp, seq, s, s_end);
+    const int kvh = c.item / p.chunks, h0 = (c.item % p.chunks) * p.chunk;
+    const int heads = min(p.chunk, p.group - h0);
+    const T* qrow = static_cast<const T*>(p.q) + (int64_t)c.n * p.q_stride + (int64_t)(kvh * p.group + h0) * DQK;
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) issue(sp, seq, kvh, s + i, s_end, i);
+    for (int i = 0; i < NT * KC / 4; ++i) {
+      const int x = i * 32 + lane, r = x / KC, ch = x % KC;
+      const uint32_t ok = r < heads;
+      cp_async16(qbuf + r * (DQK * 2) + ((ch ^ (r & 7)) << 4), qrow + (ok ? r * DQK : 0) + ch * 8, ok * 16);
+    }
+    page_next = first_page;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(c.span, c.n, kvh, c.step + i, c.s_end, i);
   };
 
-  int s_end = (int)min((int64_t)span.steps, step + left);
-  prologue(span, n, item / p.chunks, step, s_end);
+  prologue(cur, page_of(cur.span, cur.n, cur.step, cur.s_end));
 
   while (true) {
-    const int kvh = item / p.chunks, h0 = (item % p.chunks) * p.chunk;
+    const int kvh = cur.item / p.chunks, h0 = (cur.item % p.chunks) * p.chunk;
     const int heads = min(p.chunk, p.group - h0);
+    // ---- the next piece of the range, and its first page
+    left -= cur.s_end - cur.step;
+    const bool more = left > 0;
+    PagedKvPiece next = cur;
+    int next_page = -1;
+    if (more) {
+      if (++next.item == items) {
+        next.item = 0;
+        do {
+          ++next.n;
+          next.span = PagedKvSpan(p, next.n);
+        } while (next.span.steps == 0);
+      }
+      next.step = 0;
+      next.s_end = (int)min((int64_t)next.span.steps, left);
+      next_page = page_of(next.span, next.n, 0, next.s_end);
+    }
     // ---- Q^T fragments: B operand (16 d x 8 heads) per 16 columns of d
     uint32_t qf[NT][DQK / 16][2];
-    {
-      const T* qrow = static_cast<const T*>(p.q) + (int64_t)n * p.q_stride + (int64_t)(kvh * p.group + h0) * DQK;
+    cp_async_wait<S - 2>();  // the queries came with the first tile
+    __syncwarp();
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int h = t * 8 + gid;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < DQK / 16; ++k) {
-          qf[t][k][0] = qf[t][k][1] = 0u;
-          if (h < heads) {
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(qrow + (int64_t)h * DQK + k * 16 + c2);
-            qf[t][k][0] = src[0];
-            qf[t][k][1] = src[4];
-          }
-        }
+      for (int k = 0; k < DQK / 32; ++k) {
+        uint32_t a[4];
+        const int r = t * 8 + (lane & 7), ch = 4 * k + (lane >> 3);
+        ldsm4(a, qbuf + r * (DQK * 2) + ((ch ^ (r & 7)) << 4));
+        qf[t][2 * k][0] = a[0];
+        qf[t][2 * k][1] = a[1];
+        qf[t][2 * k + 1][0] = a[2];
+        qf[t][2 * k + 1][1] = a[3];
       }
-    }
     float o[NT][DV / 16][4];
     float ref[NT][2], sum[NT][2];  // heads c2, c2 + 1 of each tile of 8
 #pragma unroll
@@ -276,10 +330,10 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
     }
 
     int st = 0;
-    for (int s = step; s < s_end; ++s) {
+    for (int s = cur.step; s < cur.s_end; ++s) {
       cp_async_wait<S - 2>();
       __syncwarp();
-      issue(span, n, kvh, s + S - 1, s_end, st == 0 ? S - 1 : st - 1);
+      issue(cur.span, cur.n, kvh, s + S - 1, cur.s_end, st == 0 ? S - 1 : st - 1);
       const uint32_t vis = masks[st];
       if (vis) {
         const uint32_t kd = ring + (uint32_t)(st * L::kTileBytes), vd = kd + 16 * DQK * 2;
@@ -357,25 +411,15 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
       st = st + 1 == S ? 0 : st + 1;
     }
 
-    // ---- the next item of the range: its first tiles are asked for before
-    // this one's results are joined
-    const bool whole = step == 0 && s_end == span.steps;
-    const int slot = (int)blockIdx.x * 2 + (step == 0 ? 1 : 0);
-    const int out_n = n, out_head = kvh * p.group + h0;
-    left -= s_end - step;
-    const bool more = left > 0;
-    if (more) {
-      if (++item == items) {
-        item = 0;
-        do {
-          ++n;
-          span = PagedKvSpan(p, n);
-        } while (span.steps == 0);
-      }
-      step = 0;
-      s_end = (int)min((int64_t)span.steps, left);
-      prologue(span, n, item / p.chunks, step, s_end);
+    const bool whole = cur.step == 0 && cur.s_end == cur.span.steps;
+    const int slot = (int)blockIdx.x * 2 + (cur.step == 0 ? 1 : 0);
+    if (!more && tid == 0) {
+      // the batch's step that ends this item; its CTA c has floor(total c / ctas) <= it: c = ((it + 1) ctas - 1) / total
+      const int64_t last = end - cur.s_end + cur.span.steps - 1;
+      p.split[blockIdx.x] = make_int4(cur.step == 0 && !whole ? cur.n : -1, cur.item,
+                                      (int)(((last + 1) * ctas - 1) / total), 0);
     }
+    if (more) prologue(next, next_page);  // on its way while this item's results are joined
 
     // ---- join the four warps
 #pragma unroll
@@ -406,7 +450,7 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
         wgt[e] = ref[t][e] == m ? 1.f : ex2_approx(ref[t][e] - m);
       }
       // [warp][head][d_v], the columns of head pair c turned by 8 c: no bank conflicts
-      float* jo = join + warp * 8 * DV;
+      float* jo = staging(warp);
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k)
 #pragma unroll
@@ -429,13 +473,13 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
         float acc[8] = {};
 #pragma unroll
         for (int w = 0; w < kPkvWarps; ++w) {
-          const float4* src = reinterpret_cast<const float4*>(join + (w * 8 + h) * DV + (c8 ^ ((h >> 1) * 8)));
+          const float4* src = reinterpret_cast<const float4*>(staging(w) + h * DV + (c8 ^ ((h >> 1) * 8)));
           const float4 a = src[0], b = src[1];
           acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
           acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
         }
         if (whole) {
-          const int64_t row = (int64_t)out_n * p.n_kv * p.group + out_head + t * 8 + h;
+          const int64_t row = ((int64_t)cur.n * p.n_kv + kvh) * p.group + h0 + t * 8 + h;
           const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no keys: zeros; NaN stays NaN
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] *= inv;
@@ -454,79 +498,67 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
       __syncthreads();  // the staging area and the sums are free again
     }
     if (!more) break;
+    cur = next;
   }
 }
 
-// One CTA per item: nothing to do where a single CTA wrote it; zeros and -inf
-// where the sequence is empty; else the sum over its CTAs' parts, in order.
+// One CTA per (CTA of the first kernel, query head of its items): adds up the
+// parts of the item that begins in that CTA and ends in a later one. 16-byte
+// pieces of the row by groups of threads; each group takes every 256 / (d_v / 8)th
+// part, so a row of a few hundred parts is a few loads deep.
 template <typename T, int DV>
-__global__ void __launch_bounds__(128) decode_paged_join_kernel(const PagedKvParams p) {
-  __shared__ int64_t sh[2][4];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int items = p.n_kv * p.chunks;
-  const int n = blockIdx.y, item = blockIdx.x;
-  int64_t all = 0, before = 0;  // steps of the batch, and of the sequences before n
-  for (int i = tid; i < p.batch; i += 128) {
-    const int s = PagedKvSpan(p, i).steps;
-    all += s;
-    if (i < n) before += s;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if (lane == 0) {
-    sh[0][warp] = all;
-    sh[1][warp] = before;
-  }
-  __syncthreads();
-  all = (sh[0][0] + sh[0][1] + sh[0][2] + sh[0][3]) * items;
-  before = (sh[1][0] + sh[1][1] + sh[1][2] + sh[1][3]) * items;
-  const int steps = PagedKvSpan(p, n).steps;
-  const int kvh = item / p.chunks, h0 = (item % p.chunks) * p.chunk;
-  const int heads = min(p.chunk, p.group - h0);
-  const int64_t row0 = (int64_t)n * p.n_kv * p.group + kvh * p.group + h0;
-  // the CTA of step x of the batch is ((x + 1) ctas - 1) / total
-  int64_t c0 = 0, c1 = 0, a = 0;
-  if (steps > 0) {
-    a = before + (int64_t)item * steps;
-    const int64_t ctas = min((int64_t)p.ctas, all);
-    c0 = ((a + 1) * ctas - 1) / all;
-    c1 = ((a + steps) * ctas - 1) / all;
-  }
+__global__ void __launch_bounds__(256) decode_paged_join_kernel(const PagedKvParams p) {
+  constexpr int G = 256 / (DV / 8);  // groups of threads
+  __shared__ float red[G][DV + 4];
+  __shared__ float red_l[G], red_m[8];
+  const int tid = threadIdx.x, c8 = (tid % (DV / 8)) * 8, g = tid / (DV / 8), h = blockIdx.y;
   griddep_wait();
-  if (steps > 0 && c0 == c1) return;
-  for (int x = tid; x < heads * (DV / 8); x += 128) {
-    const int h = x / (DV / 8), c8 = (x % (DV / 8)) * 8;
-    float m = -INFINITY, l = 0.f, acc[8] = {};
-    if (steps > 0) {
-      // the first part is its CTA's slot 1 unless that CTA begins inside the item, which c0 = the
-      // CTA of the item's first step never does; every later part begins its CTA's range
-      for (int64_t c = c0; c <= c1; ++c) {
-        const int64_t row = (c * 2 + (c == c0 ? 1 : 0)) * kPkvHeads + h;
-        const float2 v = *reinterpret_cast<const float2*>(p.part_ml + row * 2);
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + row * DV + c8);
-        const float4 u = src[0], w = src[1];
-        const float mn = fmaxf(m, v.x);
-        const float fa = m == mn ? 1.f : ex2_approx(m - mn), fb = v.x == mn ? 1.f : ex2_approx(v.x - mn);
-        m = mn;
-        l = l * fa + v.y * fb;
-        acc[0] = acc[0] * fa + u.x * fb; acc[1] = acc[1] * fa + u.y * fb;
-        acc[2] = acc[2] * fa + u.z * fb; acc[3] = acc[3] * fa + u.w * fb;
-        acc[4] = acc[4] * fa + w.x * fb; acc[5] = acc[5] * fa + w.y * fb;
-        acc[6] = acc[6] * fa + w.z * fb; acc[7] = acc[7] * fa + w.w * fb;
-      }
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const int4 s = p.split[blockIdx.x];
+  if (s.x < 0) return;
+  const int kvh = s.y / p.chunks, h0 = (s.y % p.chunks) * p.chunk;
+  if (h >= min(p.chunk, p.group - h0)) return;
+  const int c0 = blockIdx.x, parts = s.z - c0 + 1;
+  // an item's first part is its CTA's slot 1 (it begins there); each later part begins its CTA's range: slot 0
+  auto row_of = [&](int j) { return ((int64_t)(c0 + j) * 2 + (j == 0 ? 1 : 0)) * kPkvHeads + h; };
+  float m = -INFINITY;
+  for (int j = tid; j < parts; j += 256) m = fmaxf(m, p.part_ml[row_of(j) * 2]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= inv;
-    const int64_t row = row0 + h;
-    *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * DV + c8) =
-        make_uint4(Mma16<T>::pack(acc[0], acc[1]), Mma16<T>::pack(acc[2], acc[3]),
-                   Mma16<T>::pack(acc[4], acc[5]), Mma16<T>::pack(acc[6], acc[7]));
-    if (c8 == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) red_m[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, red_m[w]);
+  float l = 0.f, acc[8] = {};
+#pragma unroll 4
+  for (int j = g; j < parts; j += G) {
+    const int64_t row = row_of(j);
+    const float2 v = *reinterpret_cast<const float2*>(p.part_ml + row * 2);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + row * DV + c8);
+    const float4 u = src[0], w = src[1];
+    const float f = v.x == m ? 1.f : ex2_approx(v.x - m);
+    l = fmaf(v.y, f, l);
+    acc[0] = fmaf(u.x, f, acc[0]); acc[1] = fmaf(u.y, f, acc[1]);
+    acc[2] = fmaf(u.z, f, acc[2]); acc[3] = fmaf(u.w, f, acc[3]);
+    acc[4] = fmaf(w.x, f, acc[4]); acc[5] = fmaf(w.y, f, acc[5]);
+    acc[6] = fmaf(w.z, f, acc[6]); acc[7] = fmaf(w.w, f, acc[7]);
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[g][c8 + e] = acc[e];
+  if (c8 == 0) red_l[g] = l;
+  __syncthreads();
+  if (tid >= DV / 2) return;  // two columns a thread
+  float x = 0.f, y = 0.f;
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    x += red[k][2 * tid];
+    y += red[k][2 * tid + 1];
+    l += red_l[k];
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no keys: zeros; NaN stays NaN
+  const int64_t row = ((int64_t)s.x * p.n_kv + kvh) * p.group + h0 + h;
+  reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * DV)[tid] = Mma16<T>::pack(x * inv, y * inv);
+  if (tid == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace loza

@@ -211,18 +211,18 @@ bool pkv_shape_ok(int32_t n_heads, int32_t n_kv, int32_t d_qk, int32_t d_v) {
 
 size_t pkv_part_o_bytes(int32_t d_v) { return (size_t)pkv_ctas() * 2 * kPkvHeads * d_v * sizeof(float); }
 size_t pkv_workspace_bytes(int32_t d_v) {
-  return pkv_part_o_bytes(d_v) + (size_t)pkv_ctas() * 2 * kPkvHeads * 2 * sizeof(float);
+  return pkv_part_o_bytes(d_v) + (size_t)pkv_ctas() * (2 * kPkvHeads * 2 * sizeof(float) + sizeof(int4));
 }
 
 template <typename T, int DQK, int DV, int NT>
 loza_status pkv_launch(const PagedKvParams& p, cudaStream_t st) {
   auto kernel = decode_paged_kv_kernel<T, DQK, DV, NT>;
-  constexpr int smem = PagedKvLayout<DQK, DV>::kSmem;
+  constexpr int smem = PagedKvLayout<DQK, DV, NT>::kSmem;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return LOZA_ERR_CUDA;
   kernel<<<(unsigned)p.ctas, kPkvThreads, smem, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return LOZA_ERR_CUDA;
-  if (!launch_after(decode_paged_join_kernel<T, DV>, dim3(p.n_kv * p.chunks, p.batch), 128, st, p))
+  if (!launch_after(decode_paged_join_kernel<T, DV>, dim3(p.ctas, p.chunk), 256, st, p))
     return LOZA_ERR_CUDA;
   g_launches.fetch_add(2, std::memory_order_relaxed);
   return LOZA_OK;
@@ -566,6 +566,7 @@ loza_status loza_ssa_decode_paged_kv(const void* q, int64_t q_row_stride, const 
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pkv_part_o_bytes(d_v));
   p.ctas = pkv_ctas();
+  p.split = reinterpret_cast<int4*>(p.part_ml + (size_t)p.ctas * 2 * kPkvHeads * 2);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == LOZA_BF16 ? pkv_dispatch<__nv_bfloat16>(p, d_qk, st) : pkv_dispatch<__half>(p, d_qk, st);
 }
