@@ -13,7 +13,6 @@ Tensors are torch CUDA tensors (PyTorch provides device memory and streams):
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 from ._build import LIB_PATH, build  # noqa: F401  (build is re-exported)
@@ -76,22 +75,6 @@ class Params(ctypes.Structure):
         super().__init__(block_size, n_sink, n_local, scale)
 
 
-class RopeParams(ctypes.Structure):
-    """loza_rope_params {rope_dim, rope_offset, interleaved, scale}."""
-    _fields_ = [("rope_dim", ctypes.c_int32), ("rope_offset", ctypes.c_int32),
-                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
-
-    def __init__(self, rope_dim: int, rope_offset: int = 0, interleaved: bool = False, scale: float = 1.0):
-        super().__init__(rope_dim, rope_offset, int(bool(interleaved)), scale)
-
-
-class KvPool(ctypes.Structure):
-    """loza_kv_pool: base pointers, pages and strides of a paged cache."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)] + \
-               [(f"{s}_{n}_stride", ctypes.c_int64) for s in "kv" for n in ("page", "row", "head")]
-
-
 _lib = None
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -149,28 +132,16 @@ def lib() -> ctypes.CDLL:
         L.loza_hi_decode.restype = ctypes.c_int
         L.loza_hi_decode.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _i32, _i32, Params,
                                      _i32, _i32, _vp, _vp, _vp, _sz, _vp]
-        _f32, _f64, _pool = ctypes.c_float, ctypes.c_double, ctypes.POINTER(KvPool)
-        L.loza_page_plan.restype = ctypes.c_int
-        L.loza_page_plan.argtypes = [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp,
-                                     _vp]
+        for name in ("loza_page_plan", "loza_rope", "loza_qk_norm_rope", "loza_qk_norm_rope_backward",
+                     "loza_ssa_decode_paged_kv"):  # their arguments in a struct, and the stream
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [ctypes.c_char_p, _vp]
         L.loza_rope_frequencies.restype = ctypes.c_int
-        L.loza_rope_frequencies.argtypes = [_f64, _i32, _i32, _f64, _f64, _f64, _f64, _vp, _vp]
-        L.loza_rope.restype = ctypes.c_int
-        L.loza_rope.argtypes = [_vp, _vp, _vp, _i64, _i32, _i32, _i64, RopeParams, _i32, _i32, _vp, _i64, _vp]
-        L.loza_qk_norm_rope.restype = ctypes.c_int
-        L.loza_qk_norm_rope.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i64, _i64, _i64, _vp,
-                                        _vp, _i32, _f32, RopeParams, _i32, _vp, _i64, _vp, _i64, _pool, _vp, _vp]
+        L.loza_rope_frequencies.argtypes = [ctypes.c_double, _i32, _i32] + [ctypes.c_double] * 4 + [_vp, _vp]
         L.loza_qk_norm_rope_workspace_size.restype = _sz
         L.loza_qk_norm_rope_workspace_size.argtypes = [_i32]
-        L.loza_qk_norm_rope_backward.restype = ctypes.c_int
-        L.loza_qk_norm_rope_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, _i64,
-                                                 _i64, _i64, _vp, _vp, _i32, _f32, RopeParams, _i32, _vp, _i64, _vp,
-                                                 _i64, _vp, _vp, _vp, _sz, _vp]
         L.loza_decode_paged_kv_workspace_size.restype = _sz
         L.loza_decode_paged_kv_workspace_size.argtypes = [_i32, _i32, _i32, _i32]
-        L.loza_ssa_decode_paged_kv.restype = ctypes.c_int
-        L.loza_ssa_decode_paged_kv.argtypes = [_vp, _i64, _pool, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
-                                               Params, _i32, _vp, _vp, _vp, _sz, _vp]
         _lib = L
     return _lib
 
@@ -569,345 +540,26 @@ def loza_hi_decode(q, kv_cache, q_index, k_index, page_keys, seqlens, max_seqlen
     return out, lse
 
 
-# ---------------------------------------------------------------------------
-# Serving and training around the attention: page plan, rotation, norms of
-# query and key heads, decode over paged K and V pools
-# ---------------------------------------------------------------------------
-LOZA_BF16, LOZA_FP16, LOZA_FP32 = 0, 1, 2
-LOZA_ROPE_NONE, LOZA_ROPE_LINEAR, LOZA_ROPE_NTK, LOZA_ROPE_YARN = 0, 1, 2, 3
-_ROPE_SCALING = {None: LOZA_ROPE_NONE, "none": LOZA_ROPE_NONE, "linear": LOZA_ROPE_LINEAR, "ntk": LOZA_ROPE_NTK,
-                 "yarn": LOZA_ROPE_YARN}
-_dtype_codes = {}
-
-
-def _dtype_code(t, name):
-    if not _dtype_codes:
-        import torch
-        _dtype_codes.update({torch.bfloat16: LOZA_BF16, torch.float16: LOZA_FP16, torch.float32: LOZA_FP32})
-    code = _dtype_codes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be bfloat16, float16 or float32")
-    return code
-
-
-def _on_its_device(fn):
-    """Run `fn` with the device of its first tensor current and, if `stream` is
-    given, that stream current too: buffers made inside belong to the stream
-    that uses them."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        import torch
-        first = next((a for a in args if isinstance(a, torch.Tensor)), None)
-        if first is None or not first.is_cuda:
-            raise TypeError(f"{fn.__name__}: the first tensor must be a CUDA tensor, given by position")
-        if stream is None and first.device.index == torch.cuda.current_device():
-            return fn(*args, **kw)
-        if stream is not None and stream.device != first.device:
-            raise ValueError(f"{fn.__name__}: stream and tensors are on different devices")
-        with torch.cuda.device(first.device), torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
-def _tensor(t, name, device, dtype, ndim):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions")
-    return t
-
-
-def _plain(t, name, device, dtype, shape):
-    """A contiguous tensor of exactly this dtype and shape."""
-    _tensor(t, name, device, dtype, len(shape))
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
-
-
-def _head_rows(t, name):
-    """[rows, heads, dim] with heads and dim contiguous; its row stride (of one row: any that fits)."""
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name}: heads and head dim must be contiguous within a row")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _current_stream():
-    import torch
-    return torch.cuda.current_stream().cuda_stream
-
-
-def _data(t):
-    return t.data_ptr() if t is not None else None
-
-
-def _kv_pool(k_pool, v_pool, device, dtype, n_kv, d, d_v):
-    """loza_kv_pool of [pages, rows, heads, dim] tensors (any strides, columns contiguous)."""
-    _tensor(k_pool, "k_pool", device, dtype, 4)
-    pages, rows = k_pool.shape[0], k_pool.shape[1]
-    if k_pool.shape[2] != n_kv or k_pool.shape[3] != d or (d > 1 and k_pool.stride(3) != 1):
-        raise ValueError(f"k_pool must be [pages, rows, {n_kv}, {d}] with contiguous columns")
-    pool = KvPool(k=k_pool.data_ptr(), num_pages=pages, page_size=rows, k_page_stride=k_pool.stride(0),
-                  k_row_stride=k_pool.stride(1), k_head_stride=k_pool.stride(2) if n_kv > 1 else 0)
-    if v_pool is not None:
-        _tensor(v_pool, "v_pool", device, dtype, 4)
-        if v_pool.shape != (pages, rows, n_kv, d_v) or (d_v > 1 and v_pool.stride(3) != 1):
-            raise ValueError(f"v_pool must be [{pages}, {rows}, {n_kv}, {d_v}] with contiguous columns")
-        pool.v = v_pool.data_ptr()
-        pool.v_page_stride, pool.v_row_stride = v_pool.stride(0), v_pool.stride(1)
-        pool.v_head_stride = v_pool.stride(2) if n_kv > 1 else 0
-    return pool
-
-
-@_on_its_device
-def loza_page_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, capacity: int):
-    """Block table, slots and offsets of a step of a paged cache. ctx_lens,
-    new_lens [B] int32: tokens cached and tokens appended; free_pages [F] int32:
-    pages to hand out, in order; block_table [B, columns] int32 (rows may be
-    strided), updated in place; capacity: packed rows of the step. Returns
-    (cu_seqlens [B+1] int32, seqlens [B] int32, positions [capacity] int32,
-    slots [capacity] int64, counts [3] int32: tokens, pages taken, requests
-    short of pages). Nothing is read back to the host."""
-    import torch
-    dev, i32 = ctx_lens.device, torch.int32
-    _tensor(ctx_lens, "ctx_lens", dev, i32, 1)
-    B = ctx_lens.shape[0]
-    _plain(ctx_lens, "ctx_lens", dev, i32, (B,))
-    _plain(new_lens, "new_lens", dev, i32, (B,))
-    _tensor(free_pages, "free_pages", dev, i32, 1)
-    if free_pages.shape[0] > 1 and free_pages.stride(0) != 1:
-        raise ValueError("free_pages must be contiguous")
-    _tensor(block_table, "block_table", dev, i32, 2)
-    cols = block_table.shape[1]
-    if block_table.shape[0] != B or (cols > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [batch, columns] with contiguous rows")
-    if B < 1 or capacity < 0:
-        raise LozaError(-1, "loza_page_plan")
-    small = torch.empty(2 * B + 4, dtype=i32, device=dev)  # cu_seqlens, seqlens and counts: one buffer
-    cu, lens, counts = small[:B + 1], small[B + 1:2 * B + 1], small[2 * B + 1:]
-    positions = torch.empty(capacity, dtype=i32, device=dev)
-    slots = torch.empty(capacity, dtype=torch.int64, device=dev)
-    rc = lib().loza_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(),
-                              free_pages.shape[0], page_size, block_table.data_ptr(),
-                              block_table.stride(0) if B > 1 else cols, cols, capacity, cu.data_ptr(),
-                              lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), counts.data_ptr(),
-                              _current_stream())
-    _check(rc, "loza_page_plan")
-    return cu, lens, positions, slots, counts
-
-
-def rope_frequencies(rope_dim: int, theta: float = 10000.0, scaling=None, factor: float = 1.0,
-                     original_max: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
-    """Angles per position (float64 [rope_dim / 2], on `device`) and the scale of
-    RopeParams; scaling: None, "linear", "ntk" or "yarn" (for contexts `factor`
-    times longer than original_max)."""
-    import torch
-    if scaling not in _ROPE_SCALING:
-        raise ValueError(f"scaling must be one of {[k for k in _ROPE_SCALING if k]} or None")
-    freq = torch.empty(max(0, int(rope_dim)) // 2, dtype=torch.float64)
-    scale = ctypes.c_float()
-    _check(lib().loza_rope_frequencies(float(theta), int(rope_dim), _ROPE_SCALING[scaling], float(factor),
-                                       float(original_max), float(beta_fast), float(beta_slow), freq.data_ptr(),
-                                       ctypes.addressof(scale)), "loza_rope_frequencies")
-    return (freq.to(device) if device is not None else freq), scale.value
-
-
-def _rope_tables(positions, inv_freq, rope, dev, tokens):
-    import torch
-    _plain(positions, "positions", dev, torch.int32, (tokens,))
-    _plain(inv_freq, "inv_freq", dev, torch.float64, (rope.rope_dim // 2,))
-
-
-@_on_its_device
-def loza_rope(x, positions, inv_freq, rope: RopeParams, out=None, transposed: bool = False):
-    """Position rotation of x [T, H, d] (bf16, fp16 or fp32; rows may be strided)
-    by positions [T] int32 and inv_freq [rope_dim / 2] float64. out may be x (in
-    place). transposed: the gradient (dx from dout). Returns out."""
-    import torch
-    dev, code = x.device, _dtype_code(x, "x")
-    _tensor(x, "x", dev, x.dtype, 3)
-    T, H, d = x.shape
-    _rope_tables(positions, inv_freq, rope, dev, T)
-    if out is None:
-        out = torch.empty((T, H, d), dtype=x.dtype, device=dev)
-    else:
-        _tensor(out, "out", dev, x.dtype, 3)
-        if out.shape != x.shape:
-            raise ValueError("out must have the shape of x")
-    _check(lib().loza_rope(x.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), T, H, d, _head_rows(x, "x"), rope,
-                           int(bool(transposed)), code, out.data_ptr(), _head_rows(out, "out"), _current_stream()),
-           "loza_rope")
-    return out
-
-
-def _sides(q, k, q_weight, k_weight, norm_dim):
-    """Shapes common to the norm-and-rotation calls: (device, dtype, code, T, H, Hk, d, norm_dim)."""
-    first = q if q is not None else k
-    dev, dtype, code = first.device, first.dtype, _dtype_code(first, "q or k")
-    _tensor(first, "q or k", dev, dtype, 3)
-    T, _, d = first.shape
-    for t, name in ((q, "q"), (k, "k")):
-        if t is not None:
-            _tensor(t, name, dev, dtype, 3)
-            if t.shape[0] != T or t.shape[2] != d:
-                raise ValueError("q and k must agree in tokens and head dim")
-    for w in (q_weight, k_weight):
-        if w is not None and norm_dim is None:
-            norm_dim = w.shape[0] if w.dim() == 1 else -1
-    norm_dim = 0 if norm_dim is None else int(norm_dim)
-    for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
-        if w is not None:
-            if t is None:
-                raise ValueError(f"{name} without its rows")
-            _plain(w, name, dev, dtype, (norm_dim,))
-    return dev, dtype, code, T, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], d, norm_dim
-
-
-def _like_rows(t, ref, name):
-    """`t`, or new rows like `ref`: shape and dtype checked."""
-    import torch
-    if t is None:
-        return torch.empty(ref.shape, dtype=ref.dtype, device=ref.device)
-    _tensor(t, name, ref.device, ref.dtype, 3)
-    if t.shape != ref.shape:
-        raise ValueError(f"{name} must have the shape of its input")
-    return t
-
-
-@_on_its_device
-def loza_qk_norm_rope(q, k, positions, inv_freq, rope: RopeParams, q_weight=None, k_weight=None, eps: float = 1e-6,
-                      v=None, k_pool=None, v_pool=None, slots=None, q_out=None, k_out=None, norm_dim=None):
-    """RMS norm of each head of q [T, H, d] and k [T, Hkv, d] over its first
-    norm_dim columns (default: the weights' length; a side without weight is not
-    normed), then the rotation, and - with k_pool [pages, rows, Hkv, d] and slots
-    [T] int64 - the keys (and v [T, Hkv, d_v] into v_pool) written to the paged
-    cache. q or k may be None. Returns (q_out, k_out); k_out is None when there
-    is a pool and none was given."""
-    import torch
-    dev, dtype, code, T, H, Hk, d, norm_dim = _sides(q, k, q_weight, k_weight, norm_dim)
-    _rope_tables(positions, inv_freq, rope, dev, T)
-    if q is not None:
-        q_out = _like_rows(q_out, q, "q_out")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    pool, d_v = None, 0
-    if k_pool is not None:
-        if k is None:
-            raise ValueError("k_pool without k")
-        if (v is None) != (v_pool is None):
-            raise ValueError("v and v_pool come together")
-        if v is not None:
-            _tensor(v, "v", dev, dtype, 3)
-            d_v = v.shape[2]
-            if v.shape[:2] != k.shape[:2]:
-                raise ValueError("v and k must agree in tokens and heads")
-        _plain(slots, "slots", dev, torch.int64, (T,))
-        pool = _kv_pool(k_pool, v_pool, dev, dtype, Hk, d, d_v)
-    elif v is not None or v_pool is not None or slots is not None:
-        raise ValueError("v, v_pool and slots need k_pool")
-    if k is not None and (k_pool is None or k_out is not None):
-        k_out = _like_rows(k_out, k, "k_out")
-    elif k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    row = lambda t, name: 0 if t is None else _head_rows(t, name)
-    rc = lib().loza_qk_norm_rope(
-        _data(q), _data(k), _data(v), positions.data_ptr(), inv_freq.data_ptr(), T, H, Hk, d, d_v, row(q, "q"),
-        row(k, "k"), row(v, "v"), _data(q_weight), _data(k_weight), norm_dim, eps, rope, code, _data(q_out),
-        row(q_out, "q_out"), _data(k_out), row(k_out, "k_out"), ctypes.byref(pool) if pool is not None else None,
-        _data(slots), _current_stream())
-    _check(rc, "loza_qk_norm_rope")
-    return q_out, k_out
-
-
-@_on_its_device
-def loza_qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, rope: RopeParams, q_weight=None,
-                               k_weight=None, eps: float = 1e-6, dq=None, dk=None, norm_dim=None, workspace=None):
-    """Gradient of loza_qk_norm_rope: (dq, dk, dq_weight, dk_weight) from dq_out
-    and dk_out and the forward's inputs; the weights' gradients are fp32
-    [norm_dim], None for a side without weight. A side is given (dq_out, or
-    dk_out) or None; q and k are only read where there is a weight."""
-    import torch
-    dev, dtype, code, T, H, Hk, d, norm_dim = _sides(dq_out, dk_out, q_weight, k_weight, norm_dim)
-    _rope_tables(positions, inv_freq, rope, dev, T)
-    grads = []
-    for dy, x, w, g, s in ((dq_out, q, q_weight, dq, "q"), (dk_out, k, k_weight, dk, "k")):
-        if dy is None and g is not None:
-            raise ValueError(f"d{s} without d{s}_out")
-        if w is not None:
-            if x is None:
-                raise ValueError(f"{s} is needed where there is {s}_weight")
-            _tensor(x, s, dev, dtype, 3)
-            if x.shape != dy.shape:
-                raise ValueError(f"{s} and d{s}_out must have one shape")
-        grads.append(_like_rows(g, dy, f"d{s}") if dy is not None else None)
-    dq, dk = grads
-    sums = [torch.empty(norm_dim, dtype=torch.float32, device=dev) if w is not None else None
-            for w in (q_weight, k_weight)]
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = torch.empty(lib().loza_qk_norm_rope_workspace_size(norm_dim), dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    row = lambda t, name: 0 if t is None else _head_rows(t, name)
-    qx, kx = q if q_weight is not None else None, k if k_weight is not None else None
-    rc = lib().loza_qk_norm_rope_backward(
-        _data(dq_out), _data(dk_out), _data(qx), _data(kx), positions.data_ptr(), inv_freq.data_ptr(), T, H, Hk, d,
-        row(dq_out, "dq_out"), row(dk_out, "dk_out"), row(qx, "q"), row(kx, "k"), _data(q_weight), _data(k_weight),
-        norm_dim, eps, rope, code, _data(dq), row(dq, "dq"), _data(dk), row(dk, "dk"), _data(sums[0]),
-        _data(sums[1]), _data(workspace), ws_bytes, _current_stream())
-    _check(rc, "loza_qk_norm_rope_backward")
-    return dq, dk, sums[0], sums[1]
-
-
-@_on_its_device
-def loza_ssa_decode_paged_kv(q, k_pool, v_pool, block_table, seqlens, max_seqlen: int, params: Params, out=None,
-                             lse=None, workspace=None):
-    """Decode over paged K and V pools, heads of their own or shared by groups.
-    q [B, H, d_qk] bf16 or fp16 (rows may be strided); k_pool [pages, rows, Hkv,
-    d_qk] and v_pool [pages, rows, Hkv, d_v] (any strides that are multiples of
-    16 bytes, columns contiguous); block_table [B, columns] int32; seqlens [B]
-    int32, 0 for an idle row (out 0, lse -inf). Returns (out [B, H, d_v],
-    lse [B, H])."""
-    import torch
-    dev, code = q.device, _dtype_code(q, "q")
-    _tensor(q, "q", dev, q.dtype, 3)
-    B, H, d = q.shape
-    _plain(seqlens, "seqlens", dev, torch.int32, (B,))
-    _tensor(block_table, "block_table", dev, torch.int32, 2)
-    cols = block_table.shape[1]
-    if block_table.shape[0] != B or (cols > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [batch, columns] with contiguous rows")
-    bt_stride = block_table.stride(0) if B > 1 else cols
-    page = max(1, k_pool.shape[1]) if isinstance(k_pool, torch.Tensor) and k_pool.dim() == 4 else 1
-    if cols * page < max_seqlen:
-        raise ValueError("block_table has too few columns for max_seqlen")
-    if v_pool is None:
-        raise TypeError("v_pool must be a tensor")
-    Hk, d_v = (k_pool.shape[2], v_pool.shape[3]) if k_pool.dim() == 4 and v_pool.dim() == 4 else (0, 0)
-    pool = _kv_pool(k_pool, v_pool, dev, q.dtype, Hk, d, d_v)
-    out = torch.empty((B, H, d_v), dtype=q.dtype, device=dev) if out is None else \
-        _plain(out, "out", dev, q.dtype, (B, H, d_v))
-    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if lse is None else \
-        _plain(lse, "lse", dev, torch.float32, (B, H))
-    if workspace is None:
-        workspace = torch.empty(max(16, lib().loza_decode_paged_kv_workspace_size(H, Hk, d, d_v)), dtype=torch.uint8,
-                                device=dev)
-    rc = lib().loza_ssa_decode_paged_kv(
-        q.data_ptr(), _head_rows(q, "q"), ctypes.byref(pool), block_table.data_ptr(), bt_stride, seqlens.data_ptr(),
-        B, max_seqlen, H, Hk, d, d_v, params, code, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _current_stream())
-    _check(rc, "loza_ssa_decode_paged_kv")
-    return out, lse
-
-
 def wait_selftest(limit_us: int, stream=None) -> int:
     """Launch the bounded-wait self-test (a wait that nothing completes gives
     up after limit_us); returns the status of the following device-status
     read, LOZA_ERR_TIMEOUT (-5) when the bound works."""
     _check(lib().loza_wait_selftest(int(limit_us), _stream_ptr(stream)), "loza_wait_selftest")
     return device_status(stream)
+
+
+# ---------------------------------------------------------------------------
+# Serving and training around the attention (page plan, rotation, norms of query
+# and key heads, decode over paged K and V pools): in paged.py, which needs torch
+# at import, so it is loaded when one of its names is first used.
+# ---------------------------------------------------------------------------
+_PAGED = ("LOZA_BF16", "LOZA_FP16", "LOZA_FP32", "RopeParams", "rope_frequencies", "loza_page_plan", "loza_rope",
+          "loza_qk_norm_rope", "loza_qk_norm_rope_backward", "loza_ssa_decode_paged_kv")
+
+
+def __getattr__(name):
+    if name in _PAGED:
+        from . import paged
+        globals().update({n: getattr(paged, n) for n in _PAGED})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -160,12 +160,12 @@ bool nr_run(const Params& p, int dtype, int vec, int nv, int ctas, cudaStream_t 
 // CTAs that fill the GPU: two per SM (launch bounds), one of the wide rows' instances.
 int nr_ctas(int vec, int nv) { return sm_count() * (nv * vec > 8 ? 1 : 2); }
 
-// Log2 of the warps that share a token: one warp takes whole tokens unless
-// that leaves some of `warps` without work; at most `most` of them, and never
-// more than the widest side has groups.
+// Log2 of the warps that share a token: as many as find room beside each
+// other on the GPU's `warps`; at most `most`, and never more than the widest
+// side has groups.
 int nr_wide(int64_t tokens, int64_t groups, int64_t warps, int64_t most) {
   int w = 0;
-  while ((int64_t(2) << w) <= std::min(groups, most) && (tokens << w) < warps) ++w;
+  while ((int64_t(2) << w) <= std::min(groups, most) && (tokens << (w + 1)) <= warps) ++w;
   return w;
 }
 
@@ -183,7 +183,8 @@ void nr_plan_fwd(NrFwdParams* p, int vec, int nv, int64_t groups) {
   const int64_t ctas = nr_ctas(vec, nv);
   p->wide_log = nr_wide(p->s.tokens, groups, ctas * kNrWarps, 64);
   p->parts = std::max(1, (1 << p->wide_log) / kNrWarps);
-  p->ctas = (int)std::min<int64_t>(p->s.tokens, ctas);
+  const int64_t need = ((p->s.tokens << p->wide_log) + kNrWarps - 1) / kNrWarps;  // a token or more for every warp
+  p->ctas = (int)std::max<int64_t>(1, std::min<int64_t>({p->s.tokens, ctas / p->parts, need}));
   p->batch = nr_batch(p->s, p->wide_log, 1);
 }
 
@@ -243,40 +244,40 @@ using namespace loza;
 
 extern "C" {
 
-loza_status loza_page_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t batch, const int32_t* free_pages,
-                           int32_t n_free, int32_t page_size, int32_t* block_table, int64_t bt_stride,
-                           int32_t max_pages, int64_t capacity, int32_t* cu_seqlens, int32_t* seqlens,
-                           int32_t* positions, int64_t* slots, int32_t* counts, loza_stream_t stream) {
-  if (batch < 1 || n_free < 0 || max_pages < 0 || capacity < 0 || capacity > INT32_MAX) return LOZA_ERR_INVALID_ARG;
-  if (page_size < 1 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return LOZA_ERR_INVALID_ARG;
-  if (!ctx_lens || !new_lens || !cu_seqlens || !seqlens || !counts) return LOZA_ERR_INVALID_ARG;
-  if ((n_free > 0 && !free_pages) || (max_pages > 0 && !block_table) || bt_stride < max_pages)
+loza_status loza_page_plan(const loza_page_plan_args* args, loza_stream_t stream) {
+  if (!args) return LOZA_ERR_INVALID_ARG;
+  const loza_page_plan_args a = *args;
+  if (a.batch < 1 || a.n_free < 0 || a.max_pages < 0 || a.capacity < 0 || a.capacity > INT32_MAX)
     return LOZA_ERR_INVALID_ARG;
-  if (capacity > 0 && (!positions || !slots || !aligned16(positions) || !aligned16(slots)))
+  if (a.page_size < 1 || a.page_size > 65536 || (a.page_size & (a.page_size - 1)) != 0) return LOZA_ERR_INVALID_ARG;
+  if (!a.ctx_lens || !a.new_lens || !a.cu_seqlens || !a.seqlens || !a.counts) return LOZA_ERR_INVALID_ARG;
+  if ((a.n_free > 0 && !a.free_pages) || (a.max_pages > 0 && !a.block_table) || a.bt_stride < a.max_pages)
     return LOZA_ERR_INVALID_ARG;
-  if (batch > kPlanMaxBatch) return LOZA_ERR_UNSUPPORTED;
+  if (a.capacity > 0 && (!a.positions || !a.slots || !aligned16(a.positions) || !aligned16(a.slots)))
+    return LOZA_ERR_INVALID_ARG;
+  if (a.batch > kPlanMaxBatch) return LOZA_ERR_UNSUPPORTED;
   PlanParams p{};
-  p.ctx = ctx_lens;
-  p.add = new_lens;
-  p.free_pages = free_pages;
-  p.table = block_table;
-  p.table_stride = bt_stride;
-  p.batch = batch;
-  p.max_pages = max_pages;
-  p.n_free = n_free;
-  p.page_shift = log2_of(page_size);
-  p.capacity = capacity;
-  p.cu = cu_seqlens;
-  p.seqlens = seqlens;
-  p.positions = positions;
-  p.slots = slots;
-  p.counts = counts;
-  const size_t smem = (size_t)(batch + 1) * 2 * sizeof(int);
+  p.ctx = a.ctx_lens;
+  p.add = a.new_lens;
+  p.free_pages = a.free_pages;
+  p.table = a.block_table;
+  p.table_stride = a.bt_stride;
+  p.batch = a.batch;
+  p.max_pages = a.max_pages;
+  p.n_free = a.n_free;
+  p.page_shift = log2_of(a.page_size);
+  p.capacity = a.capacity;
+  p.cu = a.cu_seqlens;
+  p.seqlens = a.seqlens;
+  p.positions = a.positions;
+  p.slots = a.slots;
+  p.counts = a.counts;
+  const size_t smem = (size_t)(a.batch + 1) * 2 * sizeof(int);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem) != cudaSuccess)
     return LOZA_ERR_CUDA;
   // four tokens a thread; new pages are at most one a request more than tokens / page_size
-  const int64_t work = std::max<int64_t>((capacity + 3) / 4, batch);
+  const int64_t work = std::max<int64_t>((a.capacity + 3) / 4, a.batch);
   const unsigned grid = (unsigned)std::max<int64_t>(
       1, std::min<int64_t>((work + kPlanThreads - 1) / kPlanThreads, (int64_t)sm_count() * 2));
   page_plan_kernel<<<grid, kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p);
@@ -321,108 +322,107 @@ loza_status loza_rope_frequencies(double theta, int32_t rope_dim, int32_t scalin
   return LOZA_OK;
 }
 
-loza_status loza_rope(const void* x, const int32_t* positions, const double* inv_freq, int64_t tokens,
-                      int32_t n_heads, int32_t d, int64_t x_row_stride, loza_rope_params rope, int32_t transposed,
-                      int32_t dtype, void* out, int64_t out_row_stride, loza_stream_t stream) {
+loza_status loza_rope(const loza_rope_args* args, loza_stream_t stream) {
+  if (!args) return LOZA_ERR_INVALID_ARG;
+  const loza_rope_args a = *args;
   NrFwdParams p{};
-  const loza_status rc = nr_shape(&p.s, tokens, d, 0, 0.f, positions, inv_freq, rope, dtype);
+  const loza_status rc = nr_shape(&p.s, a.tokens, a.d, 0, 0.f, a.positions, a.inv_freq, a.rope, a.dtype);
   if (rc != LOZA_OK) return rc;
-  if (n_heads < 1 || n_heads > 65535 || (transposed != 0 && transposed != 1)) return LOZA_ERR_INVALID_ARG;
-  if (tokens == 0) return LOZA_OK;
-  const int size = elt_size(dtype);
-  if (!nr_rows_ok(x, x_row_stride, n_heads, d, size) || !nr_rows_ok(out, out_row_stride, n_heads, d, size))
+  if (a.n_heads < 1 || a.n_heads > 65535 || (a.transposed != 0 && a.transposed != 1)) return LOZA_ERR_INVALID_ARG;
+  if (a.tokens == 0) return LOZA_OK;
+  const int size = elt_size(a.dtype);
+  if (!nr_rows_ok(a.x, a.x_row_stride, a.n_heads, a.d, size) ||
+      !nr_rows_ok(a.out, a.out_row_stride, a.n_heads, a.d, size))
     return LOZA_ERR_INVALID_ARG;
-  if (x == out && x_row_stride != out_row_stride) return LOZA_ERR_INVALID_ARG;
-  if (x == out && rope.rope_dim == 0) return LOZA_OK;
-  if (transposed) p.s.sign = -1.f;
-  p.q.x = x;
-  p.q.x_stride = x_row_stride;
-  p.q.out = out;
-  p.q.out_stride = out_row_stride;
-  p.q.heads = n_heads;
-  const int vec = nr_vec(p.s, size, {x, out}, {x_row_stride, out_row_stride});
+  if (a.x == a.out && a.x_row_stride != a.out_row_stride) return LOZA_ERR_INVALID_ARG;
+  if (a.x == a.out && a.rope.rope_dim == 0) return LOZA_OK;
+  if (a.transposed) p.s.sign = -1.f;
+  p.q.x = a.x;
+  p.q.x_stride = a.x_row_stride;
+  p.q.out = a.out;
+  p.q.out_stride = a.out_row_stride;
+  p.q.heads = a.n_heads;
+  const int vec = nr_vec(p.s, size, {a.x, a.out}, {a.x_row_stride, a.out_row_stride});
   int nv = nr_tasks(&p.s, vec);
-  if (x == out) {  // in place: the rotated columns alone
+  if (a.x == a.out) {  // in place: the rotated columns alone
     p.s.npass = 0;
     p.s.ntasks = p.s.nrope;
     p.s.lph = 1;
     while (p.s.lph * nv < p.s.ntasks) p.s.lph *= 2;
   }
-  const int64_t groups = (n_heads + 32 / p.s.lph - 1) / (32 / p.s.lph);
+  const int64_t groups = (a.n_heads + 32 / p.s.lph - 1) / (32 / p.s.lph);
   nr_plan_fwd(&p, vec, nv, groups);
-  if (!nr_run(p, dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
+  if (!nr_run(p, a.dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return LOZA_OK;
 }
 
-loza_status loza_qk_norm_rope(const void* q, const void* k, const void* v, const int32_t* positions,
-                              const double* inv_freq, int64_t tokens, int32_t n_heads, int32_t n_kv_heads, int32_t d,
-                              int32_t d_v, int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
-                              const void* q_weight, const void* k_weight, int32_t norm_dim, float eps,
-                              loza_rope_params rope, int32_t dtype, void* q_out, int64_t q_out_row_stride,
-                              void* k_out, int64_t k_out_row_stride, const loza_kv_pool* pool, const int64_t* slots,
-                              loza_stream_t stream) {
+loza_status loza_qk_norm_rope(const loza_qk_norm_rope_args* args, loza_stream_t stream) {
+  if (!args) return LOZA_ERR_INVALID_ARG;
+  const loza_qk_norm_rope_args a = *args;
+  const loza_kv_pool* pool = a.pool.k ? &a.pool : nullptr;
   NrFwdParams p{};
-  const loza_status rc = nr_shape(&p.s, tokens, d, norm_dim, eps, positions, inv_freq, rope, dtype);
+  const loza_status rc = nr_shape(&p.s, a.tokens, a.d, a.norm_dim, a.eps, a.positions, a.inv_freq, a.rope, a.dtype);
   if (rc != LOZA_OK) return rc;
-  if (n_heads < 0 || n_kv_heads < 0 || n_heads > 65535 || n_kv_heads > 65535 || n_heads + n_kv_heads < 1)
+  if (a.n_heads < 0 || a.n_kv_heads < 0 || a.n_heads > 65535 || a.n_kv_heads > 65535 || a.n_heads + a.n_kv_heads < 1)
     return LOZA_ERR_INVALID_ARG;
-  const int size = elt_size(dtype);
-  if ((q_weight || k_weight) && norm_dim < 1) return LOZA_ERR_INVALID_ARG;
-  if (!aligned_to(q_weight, size) || !aligned_to(k_weight, size)) return LOZA_ERR_INVALID_ARG;
+  const int size = elt_size(a.dtype);
+  if ((a.q_weight || a.k_weight) && a.norm_dim < 1) return LOZA_ERR_INVALID_ARG;
+  if (!aligned_to(a.q_weight, size) || !aligned_to(a.k_weight, size)) return LOZA_ERR_INVALID_ARG;
   if (pool) {
-    if (!pool_page_ok(*pool) || !pool->k || !aligned_to(pool->k, size) ||
+    if (!pool_page_ok(*pool) || !aligned_to(pool->k, size) ||
         !pool_strides_ok(pool->k_page_stride, pool->k_row_stride, pool->k_head_stride))
       return LOZA_ERR_INVALID_ARG;
-    if (n_kv_heads < 1 || (tokens > 0 && (!slots || !aligned_to(slots, 8)))) return LOZA_ERR_INVALID_ARG;
-    if ((v != nullptr) != (pool->v != nullptr)) return LOZA_ERR_INVALID_ARG;
-    if (v && (d_v < 1 || d_v > 1024 || !aligned_to(pool->v, size) ||
-              !pool_strides_ok(pool->v_page_stride, pool->v_row_stride, pool->v_head_stride)))
+    if (a.n_kv_heads < 1 || (a.tokens > 0 && (!a.slots || !aligned_to(a.slots, 8)))) return LOZA_ERR_INVALID_ARG;
+    if ((a.v != nullptr) != (pool->v != nullptr)) return LOZA_ERR_INVALID_ARG;
+    if (a.v && (a.d_v < 1 || a.d_v > 1024 || !aligned_to(pool->v, size) ||
+                !pool_strides_ok(pool->v_page_stride, pool->v_row_stride, pool->v_head_stride)))
       return LOZA_ERR_INVALID_ARG;
-  } else if (v || slots) {
+  } else if (a.v || a.slots) {
     return LOZA_ERR_INVALID_ARG;  // values and slots are for the pool
   }
-  if (n_kv_heads > 0 && !pool && !k_out) return LOZA_ERR_INVALID_ARG;
-  if (tokens == 0) return LOZA_OK;
-  if (n_heads > 0 &&
-      (!nr_rows_ok(q, q_row_stride, n_heads, d, size) || !nr_rows_ok(q_out, q_out_row_stride, n_heads, d, size)))
+  if (a.n_kv_heads > 0 && !pool && !a.k_out) return LOZA_ERR_INVALID_ARG;
+  if (a.tokens == 0) return LOZA_OK;
+  if (a.n_heads > 0 && (!nr_rows_ok(a.q, a.q_row_stride, a.n_heads, a.d, size) ||
+                        !nr_rows_ok(a.q_out, a.q_out_row_stride, a.n_heads, a.d, size)))
     return LOZA_ERR_INVALID_ARG;
-  if (n_kv_heads > 0 && (!nr_rows_ok(k, k_row_stride, n_kv_heads, d, size) ||
-                         (k_out && !nr_rows_ok(k_out, k_out_row_stride, n_kv_heads, d, size))))
+  if (a.n_kv_heads > 0 && (!nr_rows_ok(a.k, a.k_row_stride, a.n_kv_heads, a.d, size) ||
+                           (a.k_out && !nr_rows_ok(a.k_out, a.k_out_row_stride, a.n_kv_heads, a.d, size))))
     return LOZA_ERR_INVALID_ARG;
-  if (v && !nr_rows_ok(v, v_row_stride, n_kv_heads, d_v, size)) return LOZA_ERR_INVALID_ARG;
-  if ((n_heads > 0 && q == q_out && q_row_stride != q_out_row_stride) ||
-      (n_kv_heads > 0 && k == k_out && k_row_stride != k_out_row_stride))
+  if (a.v && !nr_rows_ok(a.v, a.v_row_stride, a.n_kv_heads, a.d_v, size)) return LOZA_ERR_INVALID_ARG;
+  if ((a.n_heads > 0 && a.q == a.q_out && a.q_row_stride != a.q_out_row_stride) ||
+      (a.n_kv_heads > 0 && a.k == a.k_out && a.k_row_stride != a.k_out_row_stride))
     return LOZA_ERR_INVALID_ARG;
-  if (n_heads > 0) {
-    p.q = NrSide{q, nullptr, q_weight, q_out, q_row_stride, 0, q_out_row_stride, n_heads, q == q_out && !q_weight};
+  if (a.n_heads > 0) {
+    p.q = NrSide{a.q, nullptr, a.q_weight, a.q_out, a.q_row_stride, 0, a.q_out_row_stride, a.n_heads,
+                 a.q == a.q_out && !a.q_weight};
   }
-  if (n_kv_heads > 0) {
-    p.k = NrSide{k, nullptr, k_weight, k_out, k_row_stride, 0, k_out ? k_out_row_stride : 0, n_kv_heads,
-                 k == k_out && !k_weight && !pool};
+  if (a.n_kv_heads > 0) {
+    p.k = NrSide{a.k, nullptr, a.k_weight, a.k_out, a.k_row_stride, 0, a.k_out ? a.k_out_row_stride : 0, a.n_kv_heads,
+                 a.k == a.k_out && !a.k_weight && !pool};
   }
   if (pool) {
     p.k_pool = NrPool{pool->k, pool->k_page_stride, pool->k_row_stride, pool->k_head_stride};
-    if (v) p.v_pool = NrPool{pool->v, pool->v_page_stride, pool->v_row_stride, pool->v_head_stride};
+    if (a.v) p.v_pool = NrPool{pool->v, pool->v_page_stride, pool->v_row_stride, pool->v_head_stride};
     p.page_shift = log2_of(pool->page_size);
     p.n_slots = (int64_t)pool->num_pages * pool->page_size;
-    p.slots = slots;
+    p.slots = a.slots;
   }
-  p.v = v;
-  p.v_stride = v_row_stride;
-  p.d_v = v ? d_v : 0;
+  p.v = a.v;
+  p.v_stride = a.v_row_stride;
+  p.d_v = a.v ? a.d_v : 0;
   // arguments that are not given are null or zero here and constrain nothing
   const int vec = nr_vec(p.s, size,
                          {p.q.x, p.q.out, p.q.w, p.k.x, p.k.out, p.k.w, p.k_pool.base, p.v_pool.base, p.v},
                          {p.q.x_stride, p.q.out_stride, p.k.x_stride, p.k.out_stride, p.k_pool.page_stride,
                           p.k_pool.row_stride, p.k_pool.head_stride, p.v_pool.page_stride, p.v_pool.row_stride,
-                          p.v_pool.head_stride, v ? p.v_stride : 0, p.d_v});
+                          p.v_pool.head_stride, a.v ? p.v_stride : 0, p.d_v});
   const int nv = nr_tasks(&p.s, vec);
   const int rows = 32 / p.s.lph;
   const int vper = p.d_v / vec;
   p.vper_log = vper > 0 && (vper & (vper - 1)) == 0 ? log2_of(vper) : -1;
-  nr_plan_fwd(&p, vec, nv, (std::max(n_heads, n_kv_heads) + rows - 1) / rows);
-  if (!nr_run(p, dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
+  nr_plan_fwd(&p, vec, nv, (std::max(a.n_heads, a.n_kv_heads) + rows - 1) / rows);
+  if (!nr_run(p, a.dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return LOZA_OK;
 }
@@ -432,77 +432,73 @@ size_t loza_qk_norm_rope_workspace_size(int32_t norm_dim) {
   return (size_t)2 * nr_bwd_max_ctas() * norm_dim * sizeof(float);
 }
 
-loza_status loza_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
-                                       const int32_t* positions, const double* inv_freq, int64_t tokens,
-                                       int32_t n_heads, int32_t n_kv_heads, int32_t d, int64_t dq_out_row_stride,
-                                       int64_t dk_out_row_stride, int64_t q_row_stride, int64_t k_row_stride,
-                                       const void* q_weight, const void* k_weight, int32_t norm_dim, float eps,
-                                       loza_rope_params rope, int32_t dtype, void* dq, int64_t dq_row_stride,
-                                       void* dk, int64_t dk_row_stride, float* dq_weight, float* dk_weight,
-                                       void* workspace, size_t workspace_bytes, loza_stream_t stream) {
+loza_status loza_qk_norm_rope_backward(const loza_qk_norm_rope_backward_args* args, loza_stream_t stream) {
+  if (!args) return LOZA_ERR_INVALID_ARG;
+  const loza_qk_norm_rope_backward_args a = *args;
   NrBwdParams p{};
-  const loza_status rc = nr_shape(&p.s, tokens, d, norm_dim, eps, positions, inv_freq, rope, dtype);
+  const loza_status rc = nr_shape(&p.s, a.tokens, a.d, a.norm_dim, a.eps, a.positions, a.inv_freq, a.rope, a.dtype);
   if (rc != LOZA_OK) return rc;
-  if (n_heads < 0 || n_kv_heads < 0 || n_heads > 65535 || n_kv_heads > 65535 || n_heads + n_kv_heads < 1)
+  if (a.n_heads < 0 || a.n_kv_heads < 0 || a.n_heads > 65535 || a.n_kv_heads > 65535 || a.n_heads + a.n_kv_heads < 1)
     return LOZA_ERR_INVALID_ARG;
-  const int size = elt_size(dtype);
-  if ((q_weight || k_weight) && norm_dim < 1) return LOZA_ERR_INVALID_ARG;
-  if ((q_weight && n_heads < 1) || (k_weight && n_kv_heads < 1)) return LOZA_ERR_INVALID_ARG;
-  if (!aligned_to(q_weight, size) || !aligned_to(k_weight, size)) return LOZA_ERR_INVALID_ARG;
-  if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr))
+  const int size = elt_size(a.dtype);
+  if ((a.q_weight || a.k_weight) && a.norm_dim < 1) return LOZA_ERR_INVALID_ARG;
+  if ((a.q_weight && a.n_heads < 1) || (a.k_weight && a.n_kv_heads < 1)) return LOZA_ERR_INVALID_ARG;
+  if (!aligned_to(a.q_weight, size) || !aligned_to(a.k_weight, size)) return LOZA_ERR_INVALID_ARG;
+  if ((a.q_weight != nullptr) != (a.dq_weight != nullptr) || (a.k_weight != nullptr) != (a.dk_weight != nullptr))
     return LOZA_ERR_INVALID_ARG;
-  if (!aligned_to(dq_weight, 4) || !aligned_to(dk_weight, 4)) return LOZA_ERR_INVALID_ARG;
+  if (!aligned_to(a.dq_weight, 4) || !aligned_to(a.dk_weight, 4)) return LOZA_ERR_INVALID_ARG;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (tokens == 0) {  // the weights' gradients are sums over nothing
-    if (dq_weight && cudaMemsetAsync(dq_weight, 0, (size_t)norm_dim * 4, st) != cudaSuccess) return LOZA_ERR_CUDA;
-    if (dk_weight && cudaMemsetAsync(dk_weight, 0, (size_t)norm_dim * 4, st) != cudaSuccess) return LOZA_ERR_CUDA;
+  if (a.tokens == 0) {  // the weights' gradients are sums over nothing
+    if (a.dq_weight && cudaMemsetAsync(a.dq_weight, 0, (size_t)a.norm_dim * 4, st) != cudaSuccess) return LOZA_ERR_CUDA;
+    if (a.dk_weight && cudaMemsetAsync(a.dk_weight, 0, (size_t)a.norm_dim * 4, st) != cudaSuccess) return LOZA_ERR_CUDA;
     return LOZA_OK;
   }
-  if (n_heads > 0 && (!nr_rows_ok(dq_out, dq_out_row_stride, n_heads, d, size) ||
-                      !nr_rows_ok(dq, dq_row_stride, n_heads, d, size) ||
-                      (q_weight && !nr_rows_ok(q, q_row_stride, n_heads, d, size))))
+  if (a.n_heads > 0 && (!nr_rows_ok(a.dq_out, a.dq_out_row_stride, a.n_heads, a.d, size) ||
+                        !nr_rows_ok(a.dq, a.dq_row_stride, a.n_heads, a.d, size) ||
+                        (a.q_weight && !nr_rows_ok(a.q, a.q_row_stride, a.n_heads, a.d, size))))
     return LOZA_ERR_INVALID_ARG;
-  if (n_kv_heads > 0 && (!nr_rows_ok(dk_out, dk_out_row_stride, n_kv_heads, d, size) ||
-                         !nr_rows_ok(dk, dk_row_stride, n_kv_heads, d, size) ||
-                         (k_weight && !nr_rows_ok(k, k_row_stride, n_kv_heads, d, size))))
+  if (a.n_kv_heads > 0 && (!nr_rows_ok(a.dk_out, a.dk_out_row_stride, a.n_kv_heads, a.d, size) ||
+                           !nr_rows_ok(a.dk, a.dk_row_stride, a.n_kv_heads, a.d, size) ||
+                           (a.k_weight && !nr_rows_ok(a.k, a.k_row_stride, a.n_kv_heads, a.d, size))))
     return LOZA_ERR_INVALID_ARG;
   // a gradient may replace its own input (the same rows), nothing else
-  if ((n_heads > 0 && ((dq == dq_out && dq_row_stride != dq_out_row_stride) ||
-                       (q_weight && dq == q && dq_row_stride != q_row_stride))) ||
-      (n_kv_heads > 0 && ((dk == dk_out && dk_row_stride != dk_out_row_stride) ||
-                          (k_weight && dk == k && dk_row_stride != k_row_stride))))
+  if ((a.n_heads > 0 && ((a.dq == a.dq_out && a.dq_row_stride != a.dq_out_row_stride) ||
+                         (a.q_weight && a.dq == a.q && a.dq_row_stride != a.q_row_stride))) ||
+      (a.n_kv_heads > 0 && ((a.dk == a.dk_out && a.dk_row_stride != a.dk_out_row_stride) ||
+                            (a.k_weight && a.dk == a.k && a.dk_row_stride != a.k_row_stride))))
     return LOZA_ERR_INVALID_ARG;
-  const bool sums = q_weight || k_weight;
+  const bool sums = a.q_weight || a.k_weight;
   if (sums) {
-    if (!workspace || !aligned16(workspace)) return LOZA_ERR_INVALID_ARG;
-    if (workspace_bytes < loza_qk_norm_rope_workspace_size(norm_dim)) return LOZA_ERR_WORKSPACE;
+    if (!a.workspace || !aligned16(a.workspace)) return LOZA_ERR_INVALID_ARG;
+    if (a.workspace_bytes < loza_qk_norm_rope_workspace_size(a.norm_dim)) return LOZA_ERR_WORKSPACE;
   }
   p.s.sign = -1.f;
-  if (n_heads > 0)
-    p.q = NrSide{q_weight ? q : nullptr, dq_out, q_weight, dq, q_weight ? q_row_stride : 0, dq_out_row_stride,
-                 dq_row_stride, n_heads, 0};
-  if (n_kv_heads > 0)
-    p.k = NrSide{k_weight ? k : nullptr, dk_out, k_weight, dk, k_weight ? k_row_stride : 0, dk_out_row_stride,
-                 dk_row_stride, n_kv_heads, 0};
-  p.partial = static_cast<float*>(workspace);
+  if (a.n_heads > 0)
+    p.q = NrSide{a.q_weight ? a.q : nullptr, a.dq_out, a.q_weight, a.dq, a.q_weight ? a.q_row_stride : 0,
+                 a.dq_out_row_stride, a.dq_row_stride, a.n_heads, 0};
+  if (a.n_kv_heads > 0)
+    p.k = NrSide{a.k_weight ? a.k : nullptr, a.dk_out, a.k_weight, a.dk, a.k_weight ? a.k_row_stride : 0,
+                 a.dk_out_row_stride, a.dk_row_stride, a.n_kv_heads, 0};
+  p.partial = static_cast<float*>(a.workspace);
   const int vec = nr_vec(p.s, size, {p.q.x, p.q.dy, p.q.w, p.q.out, p.k.x, p.k.dy, p.k.w, p.k.out},
                          {p.q.x_stride, p.q.dy_stride, p.q.out_stride, p.k.x_stride, p.k.dy_stride, p.k.out_stride});
   const int nv = nr_tasks(&p.s, vec);
   const int rows = 32 / p.s.lph;
-  const int64_t gq = (n_heads + rows - 1) / rows, gk = (n_kv_heads + rows - 1) / rows;
-  const int64_t ctas = std::min<int64_t>(nr_ctas(vec, nv), tokens);
-  p.wide_log = nr_wide(tokens, std::max(gq, gk), ctas * kNrWarps, kNrWarps);
+  const int64_t gq = (a.n_heads + rows - 1) / rows, gk = (a.n_kv_heads + rows - 1) / rows;
+  const int64_t full = nr_ctas(vec, nv);
+  p.wide_log = nr_wide(a.tokens, std::max(gq, gk), full * kNrWarps, kNrWarps);
+  const int64_t ctas = std::min(full, ((a.tokens << p.wide_log) + kNrWarps - 1) / kNrWarps);
   // a side of few groups is short: several tokens a warp between two barriers
   auto each = [&](int64_t groups) {
     return std::max<int64_t>(1, std::min<int64_t>(4, (int64_t(8) << p.wide_log) / std::max<int64_t>(1, groups)));
   };
   p.batch_q = nr_batch(p.s, p.wide_log, each(gq));
   p.batch_k = nr_batch(p.s, p.wide_log, each(gk));
-  if (!nr_run(p, dtype, vec, nv, (int)ctas, st)) return LOZA_ERR_CUDA;
+  if (!nr_run(p, a.dtype, vec, nv, (int)ctas, st)) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   if (sums) {
-    const NrDwParams dw{p.partial, dq_weight, dk_weight, norm_dim, (int)ctas};
-    if (!launch_after(norm_rope_dw_kernel, dim3((norm_dim + 7) / 8, 2), 512, st, dw)) return LOZA_ERR_CUDA;
+    const NrDwParams dw{p.partial, a.dq_weight, a.dk_weight, a.norm_dim, (int)ctas};
+    if (!launch_after(norm_rope_dw_kernel, dim3((a.norm_dim + 7) / 8, 2), 512, st, dw)) return LOZA_ERR_CUDA;
     g_launches.fetch_add(1, std::memory_order_relaxed);
   }
   return LOZA_OK;
@@ -513,33 +509,33 @@ size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, 
   return pkv_workspace_bytes(d_v);
 }
 
-loza_status loza_ssa_decode_paged_kv(const void* q, int64_t q_row_stride, const loza_kv_pool* pool,
-                                     const int32_t* block_table, int64_t bt_stride, const int32_t* seqlens,
-                                     int32_t batch, int32_t max_seqlen, int32_t n_heads, int32_t n_kv_heads,
-                                     int32_t d_qk, int32_t d_v, loza_ssa_params params, int32_t dtype, void* out,
-                                     float* lse, void* workspace, size_t workspace_bytes, loza_stream_t stream) {
-  if (!q || !pool || !pool->k || !pool->v || !block_table || !seqlens || !out || !lse) return LOZA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(pool->k) || !aligned16(pool->v) || !aligned16(out)) return LOZA_ERR_INVALID_ARG;
-  if (batch < 1 || batch > 65535 || max_seqlen < 1) return LOZA_ERR_INVALID_ARG;
+loza_status loza_ssa_decode_paged_kv(const loza_decode_paged_kv_args* args, loza_stream_t stream) {
+  if (!args) return LOZA_ERR_INVALID_ARG;
+  const loza_decode_paged_kv_args a = *args;
+  const loza_kv_pool* pool = &a.pool;
+  if (!a.q || !pool->k || !pool->v || !a.block_table || !a.seqlens || !a.out || !a.lse) return LOZA_ERR_INVALID_ARG;
+  if (!aligned16(a.q) || !aligned16(pool->k) || !aligned16(pool->v) || !aligned16(a.out)) return LOZA_ERR_INVALID_ARG;
+  if (a.batch < 1 || a.batch > 65535 || a.max_seqlen < 1) return LOZA_ERR_INVALID_ARG;
   if (!pool_page_ok(*pool)) return LOZA_ERR_INVALID_ARG;
   if (!pool_strides_ok(pool->k_page_stride, pool->k_row_stride, pool->k_head_stride) ||
       !pool_strides_ok(pool->v_page_stride, pool->v_row_stride, pool->v_head_stride))
     return LOZA_ERR_INVALID_ARG;
   for (int64_t s : {pool->k_page_stride, pool->k_row_stride, pool->k_head_stride, pool->v_page_stride,
-                    pool->v_row_stride, pool->v_head_stride, q_row_stride})
+                    pool->v_row_stride, pool->v_head_stride, a.q_row_stride})
     if (s % 8 != 0) return LOZA_ERR_INVALID_ARG;
-  if (n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 || n_heads > 65535) return LOZA_ERR_INVALID_ARG;
-  if (q_row_stride < (int64_t)n_heads * d_qk || q_row_stride >= (int64_t(1) << 40)) return LOZA_ERR_INVALID_ARG;
-  if (bt_stride < ((int64_t)max_seqlen + pool->page_size - 1) / pool->page_size) return LOZA_ERR_INVALID_ARG;
-  if (dtype != LOZA_BF16 && dtype != LOZA_FP16 && dtype != LOZA_FP32) return LOZA_ERR_INVALID_ARG;
-  if (!window_ok(params) || dtype == LOZA_FP32 || pool->page_size < 16 ||
-      !pkv_shape_ok(n_heads, n_kv_heads, d_qk, d_v))
+  if (a.n_heads < 1 || a.n_kv_heads < 1 || a.n_heads % a.n_kv_heads != 0 || a.n_heads > 65535)
+    return LOZA_ERR_INVALID_ARG;
+  if (a.q_row_stride < (int64_t)a.n_heads * a.d_qk || a.q_row_stride >= (int64_t(1) << 40)) return LOZA_ERR_INVALID_ARG;
+  if (a.bt_stride < ((int64_t)a.max_seqlen + pool->page_size - 1) / pool->page_size) return LOZA_ERR_INVALID_ARG;
+  if (a.dtype != LOZA_BF16 && a.dtype != LOZA_FP16 && a.dtype != LOZA_FP32) return LOZA_ERR_INVALID_ARG;
+  if (!window_ok(a.window) || a.dtype == LOZA_FP32 || pool->page_size < 16 ||
+      !pkv_shape_ok(a.n_heads, a.n_kv_heads, a.d_qk, a.d_v))
     return LOZA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned16(workspace)) return LOZA_ERR_INVALID_ARG;
-  if (workspace_bytes < pkv_workspace_bytes(d_v)) return LOZA_ERR_WORKSPACE;
+  if (!a.workspace || !aligned16(a.workspace)) return LOZA_ERR_INVALID_ARG;
+  if (a.workspace_bytes < pkv_workspace_bytes(a.d_v)) return LOZA_ERR_WORKSPACE;
   PagedKvParams p{};
-  p.q = q;
-  p.q_stride = q_row_stride;
+  p.q = a.q;
+  p.q_stride = a.q_row_stride;
   p.k = pool->k;
   p.v = pool->v;
   p.k_page = pool->k_page_stride;
@@ -548,27 +544,27 @@ loza_status loza_ssa_decode_paged_kv(const void* q, int64_t q_row_stride, const 
   p.v_page = pool->v_page_stride;
   p.v_row = pool->v_row_stride;
   p.v_head = pool->v_head_stride;
-  p.table = block_table;
-  p.table_stride = bt_stride;
-  p.seqlens = seqlens;
-  p.batch = batch;
-  p.max_seqlen = max_seqlen;
+  p.table = a.block_table;
+  p.table_stride = a.bt_stride;
+  p.seqlens = a.seqlens;
+  p.batch = a.batch;
+  p.max_seqlen = a.max_seqlen;
   p.num_pages = pool->num_pages;
   p.page_shift = log2_of(pool->page_size);
-  p.n_kv = n_kv_heads;
-  p.group = n_heads / n_kv_heads;
+  p.n_kv = a.n_kv_heads;
+  p.group = a.n_heads / a.n_kv_heads;
   p.chunks = (p.group + kPkvHeads - 1) / kPkvHeads;
   p.chunk = (p.group + p.chunks - 1) / p.chunks;
-  p.win = host_window(params);
-  p.scale_log2 = params.scale * 1.4426950408889634f;
-  p.out = out;
-  p.lse = lse;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pkv_part_o_bytes(d_v));
+  p.win = host_window(a.window);
+  p.scale_log2 = a.window.scale * 1.4426950408889634f;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.part_o = static_cast<float*>(a.workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + pkv_part_o_bytes(a.d_v));
   p.ctas = pkv_ctas();
   p.split = reinterpret_cast<int4*>(p.part_ml + (size_t)p.ctas * 2 * kPkvHeads * 2);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dtype == LOZA_BF16 ? pkv_dispatch<__nv_bfloat16>(p, d_qk, st) : pkv_dispatch<__half>(p, d_qk, st);
+  return a.dtype == LOZA_BF16 ? pkv_dispatch<__nv_bfloat16>(p, a.d_qk, st) : pkv_dispatch<__half>(p, a.d_qk, st);
 }
 
 }  // extern "C"

@@ -431,7 +431,9 @@ loza_status loza_ssa_mix(const void *o_full, const void *o_ssa, int64_t n, float
  * cache, the position rotation, norms of query and key heads, and decode over
  * paged K and V pools. (The LoZA pages name rotary dimensions (the 64 of 192
  * and 576) and paged caches only as part of the models the attention runs in;
- * these entry points are for the callers of this library.)
+ * these entry points are for the callers of this library.) They take their
+ * arguments in a struct, which is read before the call returns; the general
+ * conventions above hold (device pointers, caller's buffers, status codes).
  */
 
 /* Element types of these entry points (the other ones are bf16). */
@@ -507,11 +509,16 @@ typedef struct {
  * bt_stride; page_size a power of two up to 65,536; at most 16,384 requests
  * (LOZA_ERR_UNSUPPORTED beyond).
  */
-loza_status loza_page_plan(const int32_t *ctx_lens, const int32_t *new_lens, int32_t batch,
-                           const int32_t *free_pages, int32_t n_free, int32_t page_size,
-                           int32_t *block_table, int64_t bt_stride, int32_t max_pages, int64_t capacity,
-                           int32_t *cu_seqlens, int32_t *seqlens, int32_t *positions, int64_t *slots,
-                           int32_t *counts, loza_stream_t stream);
+typedef struct {
+    const int32_t *ctx_lens, *new_lens, *free_pages;
+    int32_t *block_table;
+    int32_t *cu_seqlens, *seqlens, *positions;
+    int64_t *slots;
+    int32_t *counts;
+    int64_t bt_stride, capacity;
+    int32_t batch, n_free, page_size, max_pages;
+} loza_page_plan_args;
+loza_status loza_page_plan(const loza_page_plan_args *args, loza_stream_t stream);
 
 /*
  * Host function: the angles per position of rope_dim / 2 pairs,
@@ -537,10 +544,17 @@ loza_status loza_rope_frequencies(double theta, int32_t rope_dim, int32_t scalin
  * one rounding. Sizes, offsets, strides and pointers that are multiples of 16
  * bytes run in 16-byte vectors; others, element by element.
  */
-loza_status loza_rope(const void *x, const int32_t *positions, const double *inv_freq, int64_t tokens,
-                      int32_t n_heads, int32_t d, int64_t x_row_stride, loza_rope_params rope,
-                      int32_t transposed, int32_t dtype, void *out, int64_t out_row_stride,
-                      loza_stream_t stream);
+typedef struct {
+    const void *x;
+    const int32_t *positions;
+    const double *inv_freq;
+    void *out;
+    int64_t tokens, x_row_stride, out_row_stride;
+    int32_t n_heads, d;
+    loza_rope_params rope;
+    int32_t transposed, dtype;
+} loza_rope_args;
+loza_status loza_rope(const loza_rope_args *args, loza_stream_t stream);
 
 /*
  * Norm of each query and key head, the rotation, and the write into a paged
@@ -556,22 +570,31 @@ loza_status loza_rope(const void *x, const int32_t *positions, const double *inv
  *   q_out, k_out  as q and k, with their own row strides; each may be its
  *             input with the same stride, or must not overlap any input.
  *             k_out may be NULL when a pool is given
- *   pool      NULL, or the cache: token t's key heads (after norm and
+ *   pool      none (pool.k NULL), or the cache: token t's key heads (after norm and
  *             rotation) and v's rows [n_kv_heads, d_v] go to row slots[t];
  *             a slot outside [0, num_pages * page_size) writes nothing.
- *             pool->v and v are both given or both NULL (the latent cache:
+ *             pool.v and v are both given or both NULL (the latent cache:
  *             d = 576, norm_dim = 512, rope_offset = 512). Slots must be
  *             distinct (except those that write nothing); every page_size
  *             from 1 on is taken here
  *   slots     device int64 [tokens] (from loza_page_plan), NULL without a pool
  */
-loza_status loza_qk_norm_rope(const void *q, const void *k, const void *v, const int32_t *positions,
-                              const double *inv_freq, int64_t tokens, int32_t n_heads, int32_t n_kv_heads,
-                              int32_t d, int32_t d_v, int64_t q_row_stride, int64_t k_row_stride,
-                              int64_t v_row_stride, const void *q_weight, const void *k_weight,
-                              int32_t norm_dim, float eps, loza_rope_params rope, int32_t dtype,
-                              void *q_out, int64_t q_out_row_stride, void *k_out, int64_t k_out_row_stride,
-                              const loza_kv_pool *pool, const int64_t *slots, loza_stream_t stream);
+typedef struct {
+    const void *q, *k, *v;
+    const int32_t *positions;
+    const double *inv_freq;
+    const void *q_weight, *k_weight;
+    void *q_out, *k_out;
+    const int64_t *slots;
+    loza_kv_pool pool;      /* pool.k NULL: none */
+    int64_t tokens;
+    int64_t q_row_stride, k_row_stride, v_row_stride, q_out_row_stride, k_out_row_stride;
+    int32_t n_heads, n_kv_heads, d, d_v, norm_dim;
+    float eps;
+    loza_rope_params rope;
+    int32_t dtype;
+} loza_qk_norm_rope_args;
+loza_status loza_qk_norm_rope(const loza_qk_norm_rope_args *args, loza_stream_t stream);
 
 /* Bytes of workspace loza_qk_norm_rope_backward needs when a weight is given (0: norm_dim out of range). */
 size_t loza_qk_norm_rope_workspace_size(int32_t norm_dim);
@@ -587,22 +610,30 @@ size_t loza_qk_norm_rope_workspace_size(int32_t norm_dim);
  *   workspace: loza_qk_norm_rope_workspace_size(norm_dim) bytes, 16-byte
  *   aligned, unless both weights are NULL; contents on entry are ignored
  */
-loza_status loza_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *q, const void *k,
-                                       const int32_t *positions, const double *inv_freq, int64_t tokens,
-                                       int32_t n_heads, int32_t n_kv_heads, int32_t d,
-                                       int64_t dq_out_row_stride, int64_t dk_out_row_stride,
-                                       int64_t q_row_stride, int64_t k_row_stride, const void *q_weight,
-                                       const void *k_weight, int32_t norm_dim, float eps,
-                                       loza_rope_params rope, int32_t dtype, void *dq, int64_t dq_row_stride,
-                                       void *dk, int64_t dk_row_stride, float *dq_weight, float *dk_weight,
-                                       void *workspace, size_t workspace_bytes, loza_stream_t stream);
+typedef struct {
+    const void *dq_out, *dk_out, *q, *k;
+    const int32_t *positions;
+    const double *inv_freq;
+    const void *q_weight, *k_weight;
+    void *dq, *dk;
+    float *dq_weight, *dk_weight;
+    void *workspace;
+    size_t workspace_bytes;
+    int64_t tokens;
+    int64_t dq_out_row_stride, dk_out_row_stride, q_row_stride, k_row_stride, dq_row_stride, dk_row_stride;
+    int32_t n_heads, n_kv_heads, d, norm_dim;
+    float eps;
+    loza_rope_params rope;
+    int32_t dtype;
+} loza_qk_norm_rope_backward_args;
+loza_status loza_qk_norm_rope_backward(const loza_qk_norm_rope_backward_args *args, loza_stream_t stream);
 
 /* Bytes of workspace loza_ssa_decode_paged_kv needs, whatever the batch and the lengths (0: unsupported shape). */
 size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, int32_t d_qk, int32_t d_v);
 
 /*
  * Decode over paged K and V pools with heads of their own or shared by groups:
- * the operation of loza_ssa_decode (window `p` at the sequence's last position,
+ * the operation of loza_ssa_decode (`window` at the sequence's last position,
  * LOZA_UNBOUNDED included) for n_heads a multiple of n_kv_heads, (d_qk, d_v) in
  * {(64,64), (128,128), (192,128)}, bf16 or fp16. The work is split over the
  * keys of all sequences together, so one long sequence and many ragged ones
@@ -625,12 +656,20 @@ size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, 
  *           aligned, contents on entry ignored; calls that can overlap on the
  *           GPU need one each
  */
-loza_status loza_ssa_decode_paged_kv(const void *q, int64_t q_row_stride, const loza_kv_pool *pool,
-                                     const int32_t *block_table, int64_t bt_stride, const int32_t *seqlens,
-                                     int32_t batch, int32_t max_seqlen, int32_t n_heads, int32_t n_kv_heads,
-                                     int32_t d_qk, int32_t d_v, loza_ssa_params p, int32_t dtype,
-                                     void *out, float *lse, void *workspace, size_t workspace_bytes,
-                                     loza_stream_t stream);
+typedef struct {
+    const void *q;
+    loza_kv_pool pool;
+    const int32_t *block_table, *seqlens;
+    void *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    int64_t q_row_stride, bt_stride;
+    int32_t batch, max_seqlen, n_heads, n_kv_heads, d_qk, d_v;
+    loza_ssa_params window;
+    int32_t dtype;
+} loza_decode_paged_kv_args;
+loza_status loza_ssa_decode_paged_kv(const loza_decode_paged_kv_args *args, loza_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char *loza_status_string(loza_status s);

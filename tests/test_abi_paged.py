@@ -1,7 +1,6 @@
 """Host-side checks of the paged operators' entry points: what they refuse before any launch, workspace
 sizes, and the frequencies, which are host arithmetic. No GPU: every call here is refused on the host or
 launches nothing."""
-import ctypes
 import math
 
 import numpy as np
@@ -9,9 +8,17 @@ import pytest
 import torch
 
 import block_sparse_streaming_b200 as bss
+from block_sparse_streaming_b200 import paged as binding
 from oracle import paged
 
-vp = ctypes.c_void_p
+
+
+def pack(args, **values):
+    """An argument struct from its fields by name; those not given are 0."""
+    assert not set(values) - set(args.names)
+    return args.pack(*[values.get(n) or 0 for n in args.names])
+
+
 INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
 
 
@@ -25,15 +32,18 @@ def _plan(L, **over):
     a = dict(ctx=1 << 20, new=1 << 21, batch=4, free=1 << 22, n_free=9, page=16, table=1 << 23, stride=8, cols=8,
              capacity=32, cu=1 << 24, lens=1 << 25, pos=1 << 26, slots=1 << 27, counts=1 << 28)
     a.update(over)
-    return L.loza_page_plan(a["ctx"], a["new"], a["batch"], a["free"], a["n_free"], a["page"], a["table"],
-                            a["stride"], a["cols"], a["capacity"], a["cu"], a["lens"], a["pos"], a["slots"],
-                            a["counts"], None)
+    return L.loza_page_plan(pack(binding.PLAN_ARGS, ctx_lens=a["ctx"], new_lens=a["new"], batch=a["batch"],
+                                 free_pages=a["free"], n_free=a["n_free"], page_size=a["page"],
+                                 block_table=a["table"], bt_stride=a["stride"], max_pages=a["cols"],
+                                 capacity=a["capacity"], cu_seqlens=a["cu"], seqlens=a["lens"], positions=a["pos"],
+                                 slots=a["slots"], counts=a["counts"]), None)
 
 
 @pytest.mark.parametrize("over,code", [
     (dict(batch=0), INVALID), (dict(batch=16385), UNSUPPORTED), (dict(page=24), INVALID), (dict(page=0), INVALID),
     (dict(page=1 << 17), INVALID), (dict(n_free=-1), INVALID), (dict(free=0), INVALID), (dict(table=0), INVALID),
-    (dict(stride=7), INVALID), (dict(cols=-1), INVALID), (dict(capacity=-1), INVALID), (dict(capacity=1 << 31), INVALID),
+    (dict(stride=7), INVALID), (dict(cols=-1), INVALID), (dict(capacity=-1), INVALID),
+    (dict(capacity=1 << 31), INVALID),
     (dict(ctx=0), INVALID), (dict(new=0), INVALID), (dict(cu=0), INVALID), (dict(lens=0), INVALID),
     (dict(counts=0), INVALID), (dict(pos=0), INVALID), (dict(slots=0), INVALID), (dict(pos=(1 << 26) + 4), INVALID),
     (dict(slots=(1 << 27) + 8), INVALID),
@@ -46,8 +56,10 @@ def test_plan_refuses(L, over, code):
 def _rope(L, rope=(64, 128, 0), **over):
     a = dict(x=1 << 20, pos=1 << 21, freq=1 << 22, T=4, H=8, d=192, xs=8 * 192, tr=0, dt=0, out=1 << 23, os=8 * 192)
     a.update(over)
-    return L.loza_rope(a["x"], a["pos"], a["freq"], a["T"], a["H"], a["d"], a["xs"],
-                       bss.RopeParams(rope[0], rope[1], rope[2]), a["tr"], a["dt"], a["out"], a["os"], None)
+    return L.loza_rope(pack(binding.ROPE_ARGS, x=a["x"], positions=a["pos"], inv_freq=a["freq"], tokens=a["T"],
+                            n_heads=a["H"], d=a["d"], x_row_stride=a["xs"], rope_dim=rope[0], rope_offset=rope[1],
+                            interleaved=rope[2], rope_scale=1.0, transposed=a["tr"], dtype=a["dt"], out=a["out"],
+                            out_row_stride=a["os"]), None)
 
 
 @pytest.mark.parametrize("rope,over,code", [
@@ -69,16 +81,14 @@ def test_rope_refuses(L, rope, over, code):
 def test_rope_of_no_tokens_launches_nothing(L):
     count = L.loza_launch_count()
     assert _rope(L, T=0, x=0, out=0, pos=0) == 0 and L.loza_launch_count() == count
-    p = bss.RopeParams(64)
-    p.interleaved = 2
-    assert L.loza_rope(1 << 20, 1 << 21, 1 << 22, 4, 8, 64, 512, p, 0, 0, 1 << 23, 512, None) == INVALID
+    assert _rope(L, (64, 128, 2)) == INVALID and L.loza_rope(None, None) == INVALID
 
 
 def _pool(**over):
-    a = dict(k=1 << 30, v=1 << 31, num_pages=10, page_size=16, k_page_stride=16 * 256, k_row_stride=256,
-             k_head_stride=128, v_page_stride=16 * 256, v_row_stride=256, v_head_stride=128)
+    a = dict(k_pool=1 << 30, v_pool=1 << 31, num_pages=10, page_size=16, k_page=16 * 256, k_row=256, k_head=128,
+             v_page=16 * 256, v_row=256, v_head=128)
     a.update(over)
-    return bss.KvPool(**a)
+    return a
 
 
 def _fwd(L, pool=None, rope=(128, 0, 0), **over):
@@ -86,10 +96,12 @@ def _fwd(L, pool=None, rope=(128, 0, 0), **over):
              vs=256, qw=1 << 24, kw=1 << 25, nd=128, eps=1e-6, dt=0, qo=1 << 26, qos=1024, ko=1 << 27, kos=256,
              slots=0)
     a.update(over)
-    return L.loza_qk_norm_rope(a["q"], a["k"], a["v"], a["pos"], a["freq"], a["T"], a["H"], a["Hk"], a["d"], a["dv"],
-                               a["qs"], a["ks"], a["vs"], a["qw"], a["kw"], a["nd"], a["eps"], bss.RopeParams(*rope),
-                               a["dt"], a["qo"], a["qos"], a["ko"], a["kos"],
-                               ctypes.byref(pool) if pool is not None else None, a["slots"], None)
+    return L.loza_qk_norm_rope(pack(
+        binding.NORM_ROPE_ARGS, q=a["q"], k=a["k"], v=a["v"], positions=a["pos"], inv_freq=a["freq"], tokens=a["T"],
+        n_heads=a["H"], n_kv_heads=a["Hk"], d=a["d"], d_v=a["dv"], q_row_stride=a["qs"], k_row_stride=a["ks"],
+        v_row_stride=a["vs"], q_weight=a["qw"], k_weight=a["kw"], norm_dim=a["nd"], eps=a["eps"], rope_dim=rope[0],
+        rope_offset=rope[1], interleaved=rope[2], rope_scale=1.0, dtype=a["dt"], q_out=a["qo"],
+        q_out_row_stride=a["qos"], k_out=a["ko"], k_out_row_stride=a["kos"], slots=a["slots"], **(pool or {})), None)
 
 
 @pytest.mark.parametrize("pool,over,code", [
@@ -100,14 +112,15 @@ def _fwd(L, pool=None, rope=(128, 0, 0), **over):
     (None, dict(v=1 << 28), INVALID), (None, dict(slots=1 << 28), INVALID),           # without a pool
     (None, dict(qo=1 << 20, qos=2048), INVALID),                                      # in place, other rows
     ({}, dict(slots=1 << 28), INVALID),                                               # a value pool without values
-    (dict(v=None), dict(v=1 << 29, slots=1 << 28), INVALID),                          # values without a pool
-    (dict(v=None), dict(), INVALID),                                                  # no slots
-    (dict(v=None), dict(slots=(1 << 28) + 4), INVALID), (dict(v=None, k=None), dict(slots=1 << 28), INVALID),
-    (dict(v=None, page_size=20), dict(slots=1 << 28), INVALID),
-    (dict(v=None, num_pages=0), dict(slots=1 << 28), INVALID),
-    (dict(v=None, num_pages=1 << 28), dict(slots=1 << 28), INVALID),                  # more rows than 31 bits
-    (dict(v=None, k_row_stride=-256), dict(slots=1 << 28), INVALID),
-    (dict(v=None), dict(slots=1 << 28, H=8, Hk=0, k=0, kw=0), INVALID),
+    (dict(v_pool=None), dict(v=1 << 29, slots=1 << 28), INVALID),                          # values without a pool
+    (dict(v_pool=None), dict(), INVALID),                                                  # no slots
+    (dict(v_pool=None), dict(slots=(1 << 28) + 4), INVALID),
+    (dict(v_pool=None, k_pool=None), dict(slots=1 << 28), INVALID),
+    (dict(v_pool=None, page_size=20), dict(slots=1 << 28), INVALID),
+    (dict(v_pool=None, num_pages=0), dict(slots=1 << 28), INVALID),
+    (dict(v_pool=None, num_pages=1 << 28), dict(slots=1 << 28), INVALID),                  # more rows than 31 bits
+    (dict(v_pool=None, k_row=-256), dict(slots=1 << 28), INVALID),
+    (dict(v_pool=None), dict(slots=1 << 28, H=8, Hk=0, k=0, kw=0), INVALID),
     ({}, dict(v=1 << 29, slots=1 << 28, dv=0), INVALID), ({}, dict(v=1 << 29, slots=1 << 28, vs=255), INVALID),
 ])
 def test_norm_rope_refuses(L, pool, over, code):
@@ -121,10 +134,13 @@ def _bwd(L, rope=(128, 0, 0), **over):
              gks=256, qs=1024, ks=256, qw=1 << 26, kw=1 << 27, nd=128, eps=1e-6, dt=0, dq=1 << 28, dqs=1024,
              dk=1 << 29, dks=256, dqw=1 << 30, dkw=(1 << 30) + 4096, ws=1 << 31, wsb=1 << 22)
     a.update(over)
-    return L.loza_qk_norm_rope_backward(
-        a["gq"], a["gk"], a["q"], a["k"], a["pos"], a["freq"], a["T"], a["H"], a["Hk"], a["d"], a["gqs"], a["gks"],
-        a["qs"], a["ks"], a["qw"], a["kw"], a["nd"], a["eps"], bss.RopeParams(*rope), a["dt"], a["dq"], a["dqs"],
-        a["dk"], a["dks"], a["dqw"], a["dkw"], a["ws"], a["wsb"], None)
+    return L.loza_qk_norm_rope_backward(pack(
+        binding.NORM_ROPE_BACKWARD_ARGS, dq_out=a["gq"], dk_out=a["gk"], q=a["q"], k=a["k"], positions=a["pos"],
+        inv_freq=a["freq"], tokens=a["T"], n_heads=a["H"], n_kv_heads=a["Hk"], d=a["d"], dq_out_row_stride=a["gqs"],
+        dk_out_row_stride=a["gks"], q_row_stride=a["qs"], k_row_stride=a["ks"], q_weight=a["qw"], k_weight=a["kw"],
+        norm_dim=a["nd"], eps=a["eps"], rope_dim=rope[0], rope_offset=rope[1], interleaved=rope[2], rope_scale=1.0,
+        dtype=a["dt"], dq=a["dq"], dq_row_stride=a["dqs"], dk=a["dk"], dk_row_stride=a["dks"], dq_weight=a["dqw"],
+        dk_weight=a["dkw"], workspace=a["ws"], workspace_bytes=a["wsb"]), None)
 
 
 @pytest.mark.parametrize("over,code", [
@@ -143,20 +159,23 @@ def _decode(L, pool={}, params=None, **over):
     a = dict(q=1 << 20, qs=1024, bt=1 << 21, bts=8, lens=1 << 22, batch=3, max_len=128, H=8, Hk=2, d=128, dv=128,
              dt=0, out=1 << 23, lse=1 << 24, ws=1 << 25, wsb=1 << 30)
     a.update(over)
-    return L.loza_ssa_decode_paged_kv(
-        a["q"], a["qs"], ctypes.byref(_pool(**pool)) if pool is not None else None, a["bt"], a["bts"], a["lens"],
-        a["batch"], a["max_len"], a["H"], a["Hk"], a["d"], a["dv"], params or bss.Params(0.1, 128, 0, -1), a["dt"],
-        a["out"], a["lse"], a["ws"], a["wsb"], None)
+    w = params or bss.Params(0.1, 128, 0, -1)
+    return L.loza_ssa_decode_paged_kv(pack(
+        binding.DECODE_ARGS, q=a["q"], q_row_stride=a["qs"], block_table=a["bt"], bt_stride=a["bts"],
+        seqlens=a["lens"], batch=a["batch"], max_seqlen=a["max_len"], n_heads=a["H"], n_kv_heads=a["Hk"],
+        d_qk=a["d"], d_v=a["dv"], block_size=w.block_size, n_sink=w.n_sink, n_local=w.n_local, scale=w.scale,
+        dtype=a["dt"], out=a["out"], lse=a["lse"], workspace=a["ws"], workspace_bytes=a["wsb"], **_pool(**pool)),
+        None)
 
 
 @pytest.mark.parametrize("pool,over,code", [
-    ({}, dict(q=0), INVALID), ({}, dict(q=(1 << 20) + 8), INVALID), (None, {}, INVALID), (dict(v=None), {}, INVALID),
-    (dict(k=None), {}, INVALID), (dict(k=(1 << 30) + 8), {}, INVALID), ({}, dict(bt=0), INVALID),
+    ({}, dict(q=0), INVALID), ({}, dict(q=(1 << 20) + 8), INVALID), (dict(v_pool=None), {}, INVALID),
+    (dict(k_pool=None), {}, INVALID), (dict(k_pool=(1 << 30) + 8), {}, INVALID), ({}, dict(bt=0), INVALID),
     ({}, dict(lens=0), INVALID), ({}, dict(out=0), INVALID), ({}, dict(lse=0), INVALID), ({}, dict(batch=0), INVALID),
     ({}, dict(batch=65536), INVALID), ({}, dict(max_len=0), INVALID), ({}, dict(max_len=129), INVALID),
     ({}, dict(bts=7), INVALID), ({}, dict(H=7), INVALID), ({}, dict(qs=1016), INVALID), ({}, dict(qs=1028), INVALID),
-    (dict(k_row_stride=260), {}, INVALID), (dict(v_head_stride=132), {}, INVALID),
-    (dict(k_page_stride=-4096), {}, INVALID), (dict(page_size=48), {}, INVALID), ({}, dict(dt=3), INVALID),
+    (dict(k_row=260), {}, INVALID), (dict(v_head=132), {}, INVALID),
+    (dict(k_page=-4096), {}, INVALID), (dict(page_size=48), {}, INVALID), ({}, dict(dt=3), INVALID),
     (dict(page_size=8), dict(bts=16), UNSUPPORTED), ({}, dict(dt=2), UNSUPPORTED),
     ({}, dict(d=96, qs=768), UNSUPPORTED), ({}, dict(d=576, dv=512, qs=8 * 576), UNSUPPORTED),
     ({}, dict(ws=0), INVALID), ({}, dict(ws=(1 << 25) + 4), INVALID), ({}, dict(wsb=4096), WORKSPACE),
