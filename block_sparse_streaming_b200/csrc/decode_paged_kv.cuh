@@ -171,16 +171,24 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
     return reinterpret_cast<float*>(pkv_smem + (w * S + S - 1) * L::kTileBytes);
   };
 
-  // ---- this CTA's range of steps, found by every warp for itself
-  const int items = p.n_kv * p.chunks;
-  int64_t total = 0;
-  for (int n0 = 0; n0 < p.batch; n0 += 32) {
-    int64_t s = n0 + lane < p.batch ? PagedKvSpan(p, n0 + lane).steps : 0;
+  // ---- this CTA's range of steps: the steps of every 32 sequences (in the ring's memory, which nothing is on
+  // its way to yet), then their running sum by every warp for itself
+  const int items = p.n_kv * p.chunks, groups = (p.batch + 31) / 32;
+  int64_t* sums = reinterpret_cast<int64_t*>(pkv_smem);
+  static_assert(65535 / 32 * 8 + 8 <= L::kRing, "a batch's sums fit the ring");
+#pragma unroll 4
+  for (int g = warp; g < groups; g += kPkvWarps) {
+    const int n0 = g * 32 + lane;
+    int64_t s = n0 < p.batch ? PagedKvSpan(p, n0).steps : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    total += s;
+    if (lane == 0) sums[g] = s * items;
   }
-  total *= items;
+  __syncthreads();
+  int64_t total = 0;
+  for (int g = lane; g < groups; g += 32) total += sums[g];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int64_t ctas = min((int64_t)p.ctas, total);  // so that no range is empty
   griddep_launch_dependents();
   // sequences without keys: their rows are nobody's item
@@ -196,10 +204,8 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
     return;
   }
   const int64_t begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
-  int n = 0;
-  int64_t before = 0;  // steps of the sequences before n
-  for (int n0 = 0; n0 < p.batch; n0 += 32) {
-    const int64_t own = n0 + lane < p.batch ? (int64_t)PagedKvSpan(p, n0 + lane).steps * items : 0;
+  // the first of 32 values whose running sum (from `before`) passes `begin`; before: the sum of those ahead of it
+  auto find = [&](int64_t own, int64_t& before) -> int {
     int64_t s = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -207,14 +213,22 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
       if (lane >= o) s += a;
     }
     const uint32_t hit = __ballot_sync(0xffffffffu, before + s > begin);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      n = n0 + l;
-      before += __shfl_sync(0xffffffffu, s - own, l);
+    const int l = hit ? __ffs(hit) - 1 : 31;
+    before += __shfl_sync(0xffffffffu, hit ? s - own : s, l);
+    return hit ? l : -1;
+  };
+  int64_t before = 0;
+  int group = 0;
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int l = find(g0 + lane < groups ? sums[g0 + lane] : 0, before);
+    if (l >= 0) {
+      group = g0 + l;
       break;
     }
-    before += __shfl_sync(0xffffffffu, s, 31);
   }
+  const int n0 = group * 32 + lane;
+  const int n = group * 32 + find(n0 < p.batch ? (int64_t)PagedKvSpan(p, n0).steps * items : 0, before);
+  __syncthreads();  // the ring is free
   PagedKvPiece cur{n, 0, 0, 0, PagedKvSpan(p, n)};
   cur.item = (int)((begin - before) / cur.span.steps);
   cur.step = (int)((begin - before) % cur.span.steps);

@@ -32,6 +32,7 @@ struct PlanParams {
 
 struct PlanRequest {
   int ctx, add, have, need;
+  PlanRequest() = default;
   __device__ __forceinline__ PlanRequest(const PlanParams& p, int r) {
     // a length outside [0, 2^30) counts as zero (sums of two stay in 31 bits)
     const int c = p.ctx[r], n = p.add[r];
@@ -66,13 +67,14 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
 
   int64_t tok0 = 0, pg0 = 0;  // sums before this chunk of requests
   int shorts = 0;
+  PlanRequest ahead{};  // of the next chunk, on its way while this one is summed
+  if (tid < p.batch) ahead = PlanRequest(p, tid);
   for (int base = 0; base < p.batch; base += kPlanThreads) {
     const int r = base + tid;
-    int add = 0, need = 0, have = 0, ctx = 0;
-    if (r < p.batch) {
-      const PlanRequest q(p, r);
-      add = q.add; need = q.need; have = q.have; ctx = q.ctx;
-    }
+    const PlanRequest q = ahead;
+    ahead = PlanRequest{};
+    if (r + kPlanThreads < p.batch) ahead = PlanRequest(p, r + kPlanThreads);
+    const int add = q.add, need = q.need, have = q.have, ctx = q.ctx;
     int64_t st = add, sp = need;  // inclusive sums over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -515,7 +515,7 @@ loza_status loza_ssa_decode_paged_kv(const loza_decode_paged_kv_args* args, loza
   const loza_kv_pool* pool = &a.pool;
   if (!a.q || !pool->k || !pool->v || !a.block_table || !a.seqlens || !a.out || !a.lse) return LOZA_ERR_INVALID_ARG;
   if (!aligned16(a.q) || !aligned16(pool->k) || !aligned16(pool->v) || !aligned16(a.out)) return LOZA_ERR_INVALID_ARG;
-  if (a.batch < 1 || a.batch > 65535 || a.max_seqlen < 1) return LOZA_ERR_INVALID_ARG;
+  if (a.batch < 1 || a.batch > 65535 || a.max_seqlen < 1 || a.max_seqlen > (1 << 30)) return LOZA_ERR_INVALID_ARG;
   if (!pool_page_ok(*pool)) return LOZA_ERR_INVALID_ARG;
   if (!pool_strides_ok(pool->k_page_stride, pool->k_row_stride, pool->k_head_stride) ||
       !pool_strides_ok(pool->v_page_stride, pool->v_row_stride, pool->v_head_stride))

@@ -161,6 +161,8 @@ def loza_page_plan(ctx_lens, new_lens, free_pages, block_table, page_size: int, 
     int32, positions [capacity] int32, slots [capacity] int64, counts [3] int32: tokens, pages taken, requests short
     of pages)."""
     i = ctx_lens.get_device()
+    if not isinstance(free_pages, _Tensor):
+        raise TypeError("free_pages must be a tensor")
     B, F = ctx_lens.numel(), free_pages.numel()
     ctx, new = _plain(ctx_lens, "ctx_lens", i, _i32, (B,)), _plain(new_lens, "new_lens", i, _i32, (B,))
     free = _plain(free_pages, "free_pages", i, _i32, (F,))

@@ -646,8 +646,8 @@ size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, 
  *           page_size). Only entries of pages that hold a key below
  *           seqlens[n] within 64 keys of the window are read. A page number
  *           outside [0, num_pages) holds no keys: they get no weight
- *   seqlens device int32 [batch], 0 <= seqlens[n] <= max_seqlen (taken to be
- *           in that range if it is not); the query of sequence n is its key
+ *   seqlens device int32 [batch], 0 <= seqlens[n] <= max_seqlen <= 2^30 (taken
+ *           to be in that range if it is not); the query of sequence n is its key
  *           seqlens[n] - 1. A sequence of length 0 (an idle row of a padded
  *           batch), or none of whose pages is there, gives out 0 and lse -inf
  *   Rows at or past seqlens[n], and rows outside the window, are not read.

@@ -172,7 +172,8 @@ def _decode(L, pool={}, params=None, **over):
     ({}, dict(q=0), INVALID), ({}, dict(q=(1 << 20) + 8), INVALID), (dict(v_pool=None), {}, INVALID),
     (dict(k_pool=None), {}, INVALID), (dict(k_pool=(1 << 30) + 8), {}, INVALID), ({}, dict(bt=0), INVALID),
     ({}, dict(lens=0), INVALID), ({}, dict(out=0), INVALID), ({}, dict(lse=0), INVALID), ({}, dict(batch=0), INVALID),
-    ({}, dict(batch=65536), INVALID), ({}, dict(max_len=0), INVALID), ({}, dict(max_len=129), INVALID),
+    ({}, dict(batch=65536), INVALID), ({}, dict(max_len=0), INVALID),
+    ({}, dict(max_len=(1 << 30) + 1, bts=1 << 30), INVALID), ({}, dict(max_len=129), INVALID),
     ({}, dict(bts=7), INVALID), ({}, dict(H=7), INVALID), ({}, dict(qs=1016), INVALID), ({}, dict(qs=1028), INVALID),
     (dict(k_row=260), {}, INVALID), (dict(v_head=132), {}, INVALID),
     (dict(k_page=-4096), {}, INVALID), (dict(page_size=48), {}, INVALID), ({}, dict(dt=3), INVALID),

@@ -469,6 +469,19 @@ def test_decode_extreme_scores(bss):
         check_decode(got, q, k, v, table, [L], (128, 0, -1), 1.0, f"decode many small {dtype}")
 
 
+@pytest.mark.parametrize("B", [32, 33, 700, 5000])
+def test_decode_of_many_sequences(bss, B):
+    """More sequences than CTAs, and than one pass of a warp over the lengths; many of them empty."""
+    g = np.random.default_rng(B)
+    lens = [int(x) for x in np.where(g.random(B) < 0.3, 0, g.integers(0, 90, B))]
+    lens[-1] = 70
+    q, k, v, table = decode_case(B, lens, 2, 1, 64, 64, 16, "bf16")
+    got = bss.loza_ssa_decode_paged_kv(q, k, v, torch.tensor(table, dtype=torch.int32, device="cuda"),
+                                       torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens),
+                                       bss.Params(0.125, 128, 0, -1))
+    check_decode(got, q, k, v, table, lens, (128, 0, -1), 0.125, f"decode of {B}")
+
+
 @pytest.mark.parametrize("layout", ["nhd", "hnd", "pair"])
 def test_decode_pool_layouts_and_strided_queries(bss, layout):
     lens, P, Hk = [513, 90, 0], 32, 3
@@ -558,6 +571,58 @@ def test_decode_is_deterministic_and_captures(bss):
     torch.cuda.synchronize()
     for st, g, qs, out, lse in runs:
         assert torch.equal(out, eager2[0]) and torch.equal(lse, eager2[1])
+
+
+def test_captured_step_at_a_fixed_capacity(bss):
+    """A whole step - plan, norm + rotation into the pool (keys in place as well), decode - captured once at a fixed
+    capacity and replayed with other lengths, against the same calls made one by one. The padded rows write nothing."""
+    B, P, H, Hk, d, cap = 6, 16, 8, 2, 128, 40
+    dt = torch.bfloat16
+    rope, params = bss.RopeParams(d), bss.Params(d ** -0.5, 128, 0, -1)
+    freq, _ = bss.rope_frequencies(d, device="cuda")
+    kw = normal(1, d, dtype=dt) + 1
+    free = torch.randperm(200, generator=torch.Generator().manual_seed(3)).int().cuda()
+    ctx, new = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2))
+
+    def state():
+        return dict(table=torch.full((B, 30), -1, dtype=torch.int32, device="cuda"),
+                    k_pool=torch.zeros(200, P, Hk, d, dtype=dt, device="cuda"),
+                    v_pool=torch.zeros(200, P, Hk, d, dtype=dt, device="cuda"))
+
+    q, k, v = normal(2, cap, H, d, dtype=dt), normal(3, cap, Hk, d, dtype=dt), normal(4, cap, Hk, d, dtype=dt)
+
+    def step(s, k_rows):
+        cu, lens, pos, slots, counts = bss.loza_page_plan(ctx, new, free, s["table"], P, cap)
+        q_out, k_out = bss.loza_qk_norm_rope(q, k_rows, pos, freq, rope, None, kw, 1e-6, v=v, k_pool=s["k_pool"],
+                                             v_pool=s["v_pool"], slots=slots, k_out=k_rows)
+        rows = q_out[(cu[1:].long() - 1).clamp(min=0)]
+        out, lse = bss.loza_ssa_decode_paged_kv(rows, s["k_pool"], s["v_pool"], s["table"], lens, 480, params)
+        return cu, lens, pos, slots, counts, q_out, k_out, out, lse
+
+    a, b, kb = state(), state(), k.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(state(), k.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = step(b, kb)
+    for seed, lengths in enumerate(([5, 0, 17, 3, 1, 9], [0, 0, 0, 0, 0, 0], [40, 0, 0, 0, 0, 0], [1, 1, 1, 1, 1, 1])):
+        new.copy_(torch.tensor(lengths, dtype=torch.int32))
+        k.copy_(normal(50 + seed, cap, Hk, d, dtype=dt))
+        kb.copy_(k)
+        ka = k.clone()
+        eager = step(a, ka)
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(eager, captured):
+            assert torch.equal(x, y)
+        assert all(torch.equal(a[n], b[n]) for n in a) and torch.equal(ka, kb)
+        n = sum(lengths)
+        assert (eager[3][n:] == -1).all() and (a["k_pool"].view(-1, Hk, d)[eager[3][:n]] == ka[:n]).all()
+        ctx.copy_(eager[1])
+        free.copy_(torch.roll(free, -int(eager[4][1])))  # what was taken goes to the end
 
 
 def test_norm_rope_on_another_stream(bss):
