@@ -48,6 +48,7 @@ constexpr int kNrWarps = kNrThreads / 32;
 
 struct NrShape {
   int d, norm_dim, rope_off, pairs, interleaved, lph, nrope, npass, ntasks;
+  int per;           // tokens whose angles a CTA forms at a time
   float scale, sign, eps, inv_norm;  // sign -1: the transposed rotation
   const double* inv_freq;
   const int32_t* positions;
@@ -154,10 +155,10 @@ struct NrTask {
 template <int VEC, bool INTER>
 __device__ __forceinline__ void nr_angles(const NrShape& s, int64_t tok0, int n, float2* tab) {
   if (s.pairs == 0) return;
-  // a thread keeps its pair (or few pairs) and walks the tokens
-  const int per = s.pairs < kNrThreads ? kNrThreads / s.pairs : 1, i0 = threadIdx.x / s.pairs;
-  if (s.pairs < kNrThreads && i0 >= per) return;
-  for (int pair = s.pairs < kNrThreads ? threadIdx.x - i0 * s.pairs : threadIdx.x; pair < s.pairs; pair += kNrThreads) {
+  // a thread keeps its pair (or few pairs) and walks the tokens, `per` of them at a time
+  const int per = s.per, i0 = s.pairs < kNrThreads ? threadIdx.x / s.pairs : 0;
+  if (i0 >= per) return;
+  for (int pair = threadIdx.x - i0 * s.pairs; pair < s.pairs; pair += kNrThreads) {
     const double freq = s.inv_freq[pair] * 0.15915494309189533577;  // turns: 1 / (2 pi)
     int t = pair / VEC, e = pair - t * VEC;
     if constexpr (INTER && VEC > 1) {
@@ -166,7 +167,7 @@ __device__ __forceinline__ void nr_angles(const NrShape& s, int64_t tok0, int n,
       e = x - t * (VEC / 2) + second * (VEC / 2);
     }
     const int at = VEC == 1 ? pair : (e >> 1) * (2 * s.nrope) + 2 * t + (e & 1);
-    for (int i = s.pairs < kNrThreads ? i0 : 0; i < n; i += per) {
+    for (int i = i0; i < n; i += per) {
       double turns = (double)s.positions[tok0 + i] * freq;
       turns -= rint(turns);
       float sn, cs;
@@ -453,20 +454,22 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
               c_lb[v] = v == 0 ? lane + 32 : kNone;
             }
           } else {
-            const NrSide& sd = c_kind == 0 ? p.q : p.k;
-            c_g = share * rows;
-            c_end = sd.heads;
-            c_hop = rows;
-            c_x = static_cast<const T*>(sd.x) + c_tok * sd.x_stride + (int64_t)(c_g + sub) * s.d;
-            c_xhop = (int64_t)(rows << p.wide_log) * s.d;
+            auto side = [&](const NrSide& sd) {
+              c_g = share * rows;
+              c_end = sd.heads;
+              c_hop = rows;
+              c_x = static_cast<const T*>(sd.x) + c_tok * sd.x_stride + (int64_t)(c_g + sub) * s.d;
+              c_xhop = (int64_t)(rows << p.wide_log) * s.d;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-              const bool on = task[v].rot || !sd.skip_pass;
-              c_oa[v] = task[v].a;
-              c_ob[v] = task[v].b;
-              c_la[v] = on && task[v].a >= 0 ? sub : kNone;
-              c_lb[v] = on && task[v].b >= 0 ? sub : kNone;
-            }
+              for (int v = 0; v < NV; ++v) {
+                const bool on = task[v].rot || !sd.skip_pass;
+                c_oa[v] = task[v].a;
+                c_ob[v] = task[v].b;
+                c_la[v] = on && task[v].a >= 0 ? sub : kNone;
+                c_lb[v] = on && task[v].b >= 0 ? sub : kNone;
+              }
+            };
+            if (c_kind == 0) side(p.q); else side(p.k);
           }
           c_hop <<= p.wide_log;
         }
@@ -522,8 +525,8 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
         page = slot >> p.page_shift;
         prow = slot & ((1 << p.page_shift) - 1);
       }
-#pragma unroll 1
-      for (int kind = 0; kind < 2; ++kind) {
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {  // unrolled: the sides' parameters at fixed places
         const NrSide& sd = kind == 0 ? p.q : p.k;
         const int heads = sd.heads, hop = rows << p.wide_log, g0 = share * rows, h = g0 + sub;
         if (g0 >= heads) continue;

@@ -56,6 +56,7 @@ loza_status nr_shape(NrShape* s, int64_t tokens, int32_t d, int32_t norm_dim, fl
   s->norm_dim = norm_dim;
   s->rope_off = r.rope_offset;
   s->pairs = r.rope_dim / 2;
+  s->per = s->pairs > 0 ? std::max(1, kNrThreads / s->pairs) : 1;
   s->interleaved = r.interleaved;
   s->scale = r.scale;
   s->sign = 1.f;
