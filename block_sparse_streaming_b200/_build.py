@@ -2,7 +2,8 @@
 
 The shared library ``libloza_ssa.so`` is written next to this file so that it
 travels with the source tree; it exposes exactly the C ABI of
-``include/loza_ssa.h``.
+``include/loza_ssa.h``. Next to it goes ``_paged_binding.so``, the compiled part
+of the Python binding (host code against torch's headers, g++).
 """
 from __future__ import annotations
 
@@ -16,6 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libloza_ssa.so")
+BINDING_PATH = os.path.join(PKG, "_paged_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -38,25 +41,49 @@ def sources():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    return _newer(LIB_PATH, sources())
+
+
+def _newer(target: str, inputs) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(s) <= os.path.getmtime(target) for s in inputs)
+
+
+def _compile(cmd, target: str, verbose: bool):
+    """Run a compiler that writes its output file (`{out}` in cmd), and put that in place in one step."""
+    tmp = target + f".tmp{os.getpid()}"
+    res = subprocess.run([tmp if c == "{out}" else c for c in cmd], capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(os.path.basename(cmd[0]) + " failed:\n" + res.stdout + res.stderr)
+    if verbose:
+        print(res.stderr)
+    os.replace(tmp, target)
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/paged_binding.cpp against the installed torch."""
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "loza_ssa.h")]
+    if not force and _newer(BINDING_PATH, inputs):
+        return BINDING_PATH
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    system = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    _compile(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-I{INCLUDE}",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+              f'-DLOZA_TORCH_VERSION="{torch.__version__}"', *[x for d in system for x in ("-isystem", d)],
+              "-o", "{out}", BINDING_SOURCE, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+              "-ltorch_python"], BINDING_PATH, verbose)
+    return BINDING_PATH
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/loza_ssa.cu (which includes every kernel) into libloza_ssa.so."""
-    if not force and up_to_date():
-        return LIB_PATH
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-o", tmp,
-           os.path.join(CSRC, "loza_ssa.cu")]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
-    if verbose:
-        print(res.stderr)
-    os.replace(tmp, LIB_PATH)
+    """Compile csrc/loza_ssa.cu (which includes every kernel) into libloza_ssa.so, and the binding."""
+    if force or not up_to_date():
+        _compile([_nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-o", "{out}",
+                  os.path.join(CSRC, "loza_ssa.cu")], LIB_PATH, verbose)
+    build_binding(force, verbose)
     return LIB_PATH
 
 

@@ -2,21 +2,47 @@
 sizes, and the frequencies, which are host arithmetic. No GPU: every call here is refused on the host or
 launches nothing."""
 import math
+import struct
 
 import numpy as np
 import pytest
 import torch
 
 import block_sparse_streaming_b200 as bss
-from block_sparse_streaming_b200 import paged as binding
 from oracle import paged
 
+
+class Args:
+    """The layout of an entry point's argument struct: names and their struct codes, in order."""
+
+    def __init__(self, *fields):
+        self.names = [n for names, _ in fields for n in names.split()]
+        self.struct = struct.Struct("@" + "".join(c * len(n.split()) for n, c in fields) + "0P")  # in whole pointers
+
+
+_POOL = (("k_pool v_pool", "P"), ("num_pages page_size", "i"), ("k_page k_row k_head v_page v_row v_head", "q"))
+_ROPE = (("rope_dim rope_offset interleaved", "i"), ("rope_scale", "f"))
+PLAN_ARGS = Args(("ctx_lens new_lens free_pages block_table cu_seqlens seqlens positions slots counts", "P"),
+                 ("bt_stride capacity", "q"), ("batch n_free page_size max_pages", "i"))
+ROPE_ARGS = Args(("x positions inv_freq out", "P"), ("tokens x_row_stride out_row_stride", "q"), ("n_heads d", "i"),
+                 *_ROPE, ("transposed dtype", "i"))
+NORM_ROPE_ARGS = Args(("q k v positions inv_freq q_weight k_weight q_out k_out slots", "P"), *_POOL,
+                      ("tokens q_row_stride k_row_stride v_row_stride q_out_row_stride k_out_row_stride", "q"),
+                      ("n_heads n_kv_heads d d_v norm_dim", "i"), ("eps", "f"), *_ROPE, ("dtype", "i"))
+NORM_ROPE_BACKWARD_ARGS = Args(
+    ("dq_out dk_out q k positions inv_freq q_weight k_weight dq dk dq_weight dk_weight workspace", "P"),
+    ("workspace_bytes", "N"),
+    ("tokens dq_out_row_stride dk_out_row_stride q_row_stride k_row_stride dq_row_stride dk_row_stride", "q"),
+    ("n_heads n_kv_heads d norm_dim", "i"), ("eps", "f"), *_ROPE, ("dtype", "i"))
+DECODE_ARGS = Args(("q", "P"), *_POOL, ("block_table seqlens out lse workspace", "P"), ("workspace_bytes", "N"),
+                   ("q_row_stride bt_stride", "q"), ("batch max_seqlen n_heads n_kv_heads d_qk d_v", "i"),
+                   ("block_size n_sink n_local", "i"), ("scale", "f"), ("dtype", "i"))
 
 
 def pack(args, **values):
     """An argument struct from its fields by name; those not given are 0."""
     assert not set(values) - set(args.names)
-    return args.pack(*[values.get(n) or 0 for n in args.names])
+    return args.struct.pack(*[values.get(n) or 0 for n in args.names])
 
 
 INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
@@ -32,7 +58,7 @@ def _plan(L, **over):
     a = dict(ctx=1 << 20, new=1 << 21, batch=4, free=1 << 22, n_free=9, page=16, table=1 << 23, stride=8, cols=8,
              capacity=32, cu=1 << 24, lens=1 << 25, pos=1 << 26, slots=1 << 27, counts=1 << 28)
     a.update(over)
-    return L.loza_page_plan(pack(binding.PLAN_ARGS, ctx_lens=a["ctx"], new_lens=a["new"], batch=a["batch"],
+    return L.loza_page_plan(pack(PLAN_ARGS, ctx_lens=a["ctx"], new_lens=a["new"], batch=a["batch"],
                                  free_pages=a["free"], n_free=a["n_free"], page_size=a["page"],
                                  block_table=a["table"], bt_stride=a["stride"], max_pages=a["cols"],
                                  capacity=a["capacity"], cu_seqlens=a["cu"], seqlens=a["lens"], positions=a["pos"],
@@ -56,7 +82,7 @@ def test_plan_refuses(L, over, code):
 def _rope(L, rope=(64, 128, 0), **over):
     a = dict(x=1 << 20, pos=1 << 21, freq=1 << 22, T=4, H=8, d=192, xs=8 * 192, tr=0, dt=0, out=1 << 23, os=8 * 192)
     a.update(over)
-    return L.loza_rope(pack(binding.ROPE_ARGS, x=a["x"], positions=a["pos"], inv_freq=a["freq"], tokens=a["T"],
+    return L.loza_rope(pack(ROPE_ARGS, x=a["x"], positions=a["pos"], inv_freq=a["freq"], tokens=a["T"],
                             n_heads=a["H"], d=a["d"], x_row_stride=a["xs"], rope_dim=rope[0], rope_offset=rope[1],
                             interleaved=rope[2], rope_scale=1.0, transposed=a["tr"], dtype=a["dt"], out=a["out"],
                             out_row_stride=a["os"]), None)
@@ -97,7 +123,7 @@ def _fwd(L, pool=None, rope=(128, 0, 0), **over):
              slots=0)
     a.update(over)
     return L.loza_qk_norm_rope(pack(
-        binding.NORM_ROPE_ARGS, q=a["q"], k=a["k"], v=a["v"], positions=a["pos"], inv_freq=a["freq"], tokens=a["T"],
+        NORM_ROPE_ARGS, q=a["q"], k=a["k"], v=a["v"], positions=a["pos"], inv_freq=a["freq"], tokens=a["T"],
         n_heads=a["H"], n_kv_heads=a["Hk"], d=a["d"], d_v=a["dv"], q_row_stride=a["qs"], k_row_stride=a["ks"],
         v_row_stride=a["vs"], q_weight=a["qw"], k_weight=a["kw"], norm_dim=a["nd"], eps=a["eps"], rope_dim=rope[0],
         rope_offset=rope[1], interleaved=rope[2], rope_scale=1.0, dtype=a["dt"], q_out=a["qo"],
@@ -135,7 +161,7 @@ def _bwd(L, rope=(128, 0, 0), **over):
              dk=1 << 29, dks=256, dqw=1 << 30, dkw=(1 << 30) + 4096, ws=1 << 31, wsb=1 << 22)
     a.update(over)
     return L.loza_qk_norm_rope_backward(pack(
-        binding.NORM_ROPE_BACKWARD_ARGS, dq_out=a["gq"], dk_out=a["gk"], q=a["q"], k=a["k"], positions=a["pos"],
+        NORM_ROPE_BACKWARD_ARGS, dq_out=a["gq"], dk_out=a["gk"], q=a["q"], k=a["k"], positions=a["pos"],
         inv_freq=a["freq"], tokens=a["T"], n_heads=a["H"], n_kv_heads=a["Hk"], d=a["d"], dq_out_row_stride=a["gqs"],
         dk_out_row_stride=a["gks"], q_row_stride=a["qs"], k_row_stride=a["ks"], q_weight=a["qw"], k_weight=a["kw"],
         norm_dim=a["nd"], eps=a["eps"], rope_dim=rope[0], rope_offset=rope[1], interleaved=rope[2], rope_scale=1.0,
@@ -161,7 +187,7 @@ def _decode(L, pool={}, params=None, **over):
     a.update(over)
     w = params or bss.Params(0.1, 128, 0, -1)
     return L.loza_ssa_decode_paged_kv(pack(
-        binding.DECODE_ARGS, q=a["q"], q_row_stride=a["qs"], block_table=a["bt"], bt_stride=a["bts"],
+        DECODE_ARGS, q=a["q"], q_row_stride=a["qs"], block_table=a["bt"], bt_stride=a["bts"],
         seqlens=a["lens"], batch=a["batch"], max_seqlen=a["max_len"], n_heads=a["H"], n_kv_heads=a["Hk"],
         d_qk=a["d"], d_v=a["dv"], block_size=w.block_size, n_sink=w.n_sink, n_local=w.n_local, scale=w.scale,
         dtype=a["dt"], out=a["out"], lse=a["lse"], workspace=a["ws"], workspace_bytes=a["wsb"], **_pool(**pool)),
