@@ -88,7 +88,7 @@ struct NrBwdParams {
   NrShape s;
   NrSide q, k;
   float* partial;       // [2][gridDim.x][norm_dim]
-  int batch_q, batch_k; // tokens per step of a CTA
+  int batch;            // tokens per step of a CTA
   int wide_log;
 };
 
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ba
     const NrSide& sd = side == 0 ? p.q : p.k;
     const int heads = sd.heads;
     if (heads == 0) continue;
-    const int batch = side == 0 ? p.batch_q : p.batch_k;
+    const int batch = p.batch;
     const int table_size = batch * s.pairs, hop = rows << p.wide_log, g0 = share * rows;
     const int64_t xhop = (int64_t)hop * s.d;
     const T* w = static_cast<const T*>(sd.w);

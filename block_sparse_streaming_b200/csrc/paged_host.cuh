@@ -95,8 +95,9 @@ int nr_tasks(NrShape* s, int vec) {
   return nv;
 }
 
-// Angles of a batch, at most: eight tokens of the longest table (512 pairs) fit, so a warp always has its token.
-constexpr int64_t kNrTableBytes = kNrWarps * 512 * sizeof(float2);
+// Angles of a batch: 16 KB lets two CTAs and their rings share an SM; one token per warp of the longest table (512
+// pairs, 32 KB) always fits, on an SM of its own (rows that long run one CTA per SM anyway).
+constexpr int64_t kNrTableBytes = 16384;
 
 template <typename T, int VEC, int NV, bool NORM, bool INTER>
 bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
@@ -113,7 +114,7 @@ template <typename T, int VEC, int NV, bool INTER>
 bool nr_launch_bwd(const NrBwdParams& p, int ctas, cudaStream_t st) {
   auto kernel = norm_rope_backward_kernel<T, VEC, NV, INTER>;
   const size_t smem = NrRing<VEC, NV, 2>::kBytes +
-                      std::max((size_t)2 * std::max(p.batch_q, p.batch_k) * p.s.pairs * sizeof(float2),
+                      std::max((size_t)2 * p.batch * p.s.pairs * sizeof(float2),
                                (size_t)kNrWarps * p.s.norm_dim * sizeof(float));
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -170,12 +171,15 @@ int nr_wide(int64_t tokens, int64_t groups, int64_t warps, int64_t most) {
   return w;
 }
 
-// Tokens per step of a CTA: `each` per warp (or group of warps), as far as the angles fit.
-int nr_batch(const NrShape& s, int wide_log, int64_t each) {
-  const int64_t step = std::max(1, kNrWarps >> wide_log);
-  int64_t b = step * each;
-  if (s.pairs > 0) b = std::min<int64_t>(b, kNrTableBytes / ((int64_t)s.pairs * sizeof(float2)));
-  return (int)(b / step * step);
+// Tokens per step of a CTA, between two barriers: four per warp (or group of
+// warps) as far as the angles fit. One per warp instead of four: norm +
+// rotation of 16,381 tokens 78 against 75 us, the gradient of 32,749 201
+// against 195.
+int nr_batch(const NrShape& s, int wide_log) {
+  const int step = std::max(1, kNrWarps >> wide_log);
+  int each = 4;
+  while (each > 1 && (int64_t)step * each * s.pairs * (int64_t)sizeof(float2) > kNrTableBytes) each /= 2;
+  return step * each;
 }
 
 // The forward's walk, from the groups of the widest side. With fewer tokens
@@ -186,7 +190,7 @@ void nr_plan_fwd(NrFwdParams* p, int vec, int nv, int64_t groups) {
   p->parts = std::max(1, (1 << p->wide_log) / kNrWarps);
   const int64_t need = ((p->s.tokens << p->wide_log) + kNrWarps - 1) / kNrWarps;  // a token or more for every warp
   p->ctas = (int)std::max<int64_t>(1, std::min<int64_t>({p->s.tokens, ctas / p->parts, need}));
-  p->batch = nr_batch(p->s, p->wide_log, 1);
+  p->batch = nr_batch(p->s, p->wide_log);
 }
 
 // CTAs of the backward at most (the workspace holds a row of sums per side for each).
@@ -489,12 +493,7 @@ loza_status loza_qk_norm_rope_backward(const loza_qk_norm_rope_backward_args* ar
   const int64_t full = nr_ctas(vec, nv);
   p.wide_log = nr_wide(a.tokens, std::max(gq, gk), full * kNrWarps, kNrWarps);
   const int64_t ctas = std::min(full, ((a.tokens << p.wide_log) + kNrWarps - 1) / kNrWarps);
-  // a side of few groups is short: several tokens a warp between two barriers
-  auto each = [&](int64_t groups) {
-    return std::max<int64_t>(1, std::min<int64_t>(4, (int64_t(8) << p.wide_log) / std::max<int64_t>(1, groups)));
-  };
-  p.batch_q = nr_batch(p.s, p.wide_log, each(gq));
-  p.batch_k = nr_batch(p.s, p.wide_log, each(gk));
+  p.batch = nr_batch(p.s, p.wide_log);
   if (!nr_run(p, a.dtype, vec, nv, (int)ctas, st)) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   if (sums) {
