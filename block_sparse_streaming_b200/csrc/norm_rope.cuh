@@ -47,7 +47,7 @@ constexpr int kNrThreads = 256;
 constexpr int kNrWarps = kNrThreads / 32;
 
 struct NrShape {
-  int d, norm_dim, rope_off, pairs, interleaved, lph, nrope, npass, ntasks;
+  int d, norm_dim, rope_off, pairs, interleaved, lph, lph_log, nrope, npass, ntasks;
   int per;           // tokens whose angles a CTA forms at a time
   float scale, sign, eps, inv_norm;  // sign -1: the transposed rotation
   const double* inv_freq;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
   const uint32_t ring_addr = smem_u32(ring);
   int64_t begin, end;
   nr_share(s, blockIdx.x / p.parts, p.ctas, begin, end);
-  const int lph = s.lph, t0 = lane & (lph - 1), sub = lane / lph, rows = 32 / lph;
+  const int lph = 1 << s.lph_log, t0 = lane & (lph - 1), sub = lane >> s.lph_log, rows = 32 >> s.lph_log;
   NrTask<VEC> task[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) task[v] = NrTask<VEC>(s, t0 + v * lph);
@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
 #pragma unroll 1
     for (int k = 0; k < Ring::kAhead; ++k) ask();
   }
+  int64_t slot_next = p.slots && begin + tok_first < end ? p.slots[begin + tok_first] : -1;  // of this warp's next token
   nr_angles<VEC, INTER>(s, begin, (int)min((int64_t)p.batch, end - begin), tables);
 
   int turn = 0;
@@ -517,14 +518,10 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
     const float2* tab = tables + turn * table_size;
     for (int i = tok_first; i < n; i += tok_step) {
       const int64_t tok = tok0 + i;
-      int64_t page = 0, prow = 0;
-      bool pooled = false;
-      if (p.slots) {
-        const int64_t slot = p.slots[tok];
-        pooled = slot >= 0 && slot < p.n_slots;  // else a padded row, or a page that is not there
-        page = slot >> p.page_shift;
-        prow = slot & ((1 << p.page_shift) - 1);
-      }
+      const int64_t slot = slot_next;
+      if (p.slots) slot_next = tok + tok_step < end ? p.slots[tok + tok_step] : -1;
+      const bool pooled = slot >= 0 && slot < p.n_slots;  // else a padded row, or a page that is not there
+      const int64_t page = slot >> p.page_shift, prow = slot & ((1 << p.page_shift) - 1);
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {  // unrolled: the sides' parameters at fixed places
         const NrSide& sd = kind == 0 ? p.q : p.k;

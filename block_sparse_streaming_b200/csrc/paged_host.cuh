@@ -90,8 +90,9 @@ int nr_tasks(NrShape* s, int vec) {
   s->ntasks = s->nrope + (s->npass + 1) / 2;
   int nv = vec == 1 ? 4 : 1;
   while (nv * 32 < s->ntasks) nv = vec == 1 ? 16 : nv * 2;
-  s->lph = 1;
-  while (s->lph * nv < s->ntasks) s->lph *= 2;
+  s->lph_log = 0;
+  while ((nv << s->lph_log) < s->ntasks) ++s->lph_log;
+  s->lph = 1 << s->lph_log;
   return nv;
 }
 
@@ -352,10 +353,12 @@ loza_status loza_rope(const loza_rope_args* args, loza_stream_t stream) {
   if (a.x == a.out) {  // in place: the rotated columns alone
     p.s.npass = 0;
     p.s.ntasks = p.s.nrope;
-    p.s.lph = 1;
-    while (p.s.lph * nv < p.s.ntasks) p.s.lph *= 2;
+    p.s.lph_log = 0;
+    while ((nv << p.s.lph_log) < p.s.ntasks) ++p.s.lph_log;
+    p.s.lph = 1 << p.s.lph_log;
   }
-  const int64_t groups = (a.n_heads + 32 / p.s.lph - 1) / (32 / p.s.lph);
+  const int rows = 32 >> p.s.lph_log;
+  const int64_t groups = (a.n_heads + rows - 1) / rows;
   nr_plan_fwd(&p, vec, nv, groups);
   if (!nr_run(p, a.dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
@@ -423,7 +426,7 @@ loza_status loza_qk_norm_rope(const loza_qk_norm_rope_args* args, loza_stream_t 
                           p.k_pool.row_stride, p.k_pool.head_stride, p.v_pool.page_stride, p.v_pool.row_stride,
                           p.v_pool.head_stride, a.v ? p.v_stride : 0, p.d_v});
   const int nv = nr_tasks(&p.s, vec);
-  const int rows = 32 / p.s.lph;
+  const int rows = 32 >> p.s.lph_log;
   const int vper = p.d_v / vec;
   p.vper_log = vper > 0 && (vper & (vper - 1)) == 0 ? log2_of(vper) : -1;
   nr_plan_fwd(&p, vec, nv, (std::max(a.n_heads, a.n_kv_heads) + rows - 1) / rows);
@@ -488,7 +491,7 @@ loza_status loza_qk_norm_rope_backward(const loza_qk_norm_rope_backward_args* ar
   const int vec = nr_vec(p.s, size, {p.q.x, p.q.dy, p.q.w, p.q.out, p.k.x, p.k.dy, p.k.w, p.k.out},
                          {p.q.x_stride, p.q.dy_stride, p.q.out_stride, p.k.x_stride, p.k.dy_stride, p.k.out_stride});
   const int nv = nr_tasks(&p.s, vec);
-  const int rows = 32 / p.s.lph;
+  const int rows = 32 >> p.s.lph_log;
   const int64_t gq = (a.n_heads + rows - 1) / rows, gk = (a.n_kv_heads + rows - 1) / rows;
   const int64_t full = nr_ctas(vec, nv);
   p.wide_log = nr_wide(a.tokens, std::max(gq, gk), full * kNrWarps, kNrWarps);
