@@ -264,13 +264,13 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
         for (int i = 0; i < KC / 2; ++i) {
           const int x = i * 32 + lane, r = x / KC, c = x % KC;
           const uint32_t ok = (vis >> r) & 1u;
-          cp_async16(kd + r * (DQK * 2) + ((c ^ (r & 7)) << 4), ks + (ok ? r : 0) * p.k_row + c * 8, ok * 16);
+          cp_async<16>(kd + r * (DQK * 2) + ((c ^ (r & 7)) << 4), ks + (ok ? r : 0) * p.k_row + c * 8, ok * 16);
         }
 #pragma unroll
         for (int i = 0; i < VC / 2; ++i) {
           const int x = i * 32 + lane, r = x / VC, c = x % VC;
           const uint32_t ok = (vis >> r) & 1u;
-          cp_async16(vd + r * (DV * 2) + ((c ^ (r & 7)) << 4), vs + (ok ? r : 0) * p.v_row + c * 8, ok * 16);
+          cp_async<16>(vd + r * (DV * 2) + ((c ^ (r & 7)) << 4), vs + (ok ? r : 0) * p.v_row + c * 8, ok * 16);
         }
       }
     }
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
     for (int i = 0; i < NT * KC / 4; ++i) {
       const int x = i * 32 + lane, r = x / KC, ch = x % KC;
       const uint32_t ok = r < heads;
-      cp_async16(qbuf + r * (DQK * 2) + ((ch ^ (r & 7)) << 4), qrow + (ok ? r * DQK : 0) + ch * 8, ok * 16);
+      cp_async<16>(qbuf + r * (DQK * 2) + ((ch ^ (r & 7)) << 4), qrow + (ok ? r * DQK : 0) + ch * 8, ok * 16);
     }
     page_next = first_page;
 #pragma unroll
@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
     const bool whole = cur.step == 0 && cur.s_end == cur.span.steps;
     const int slot = (int)blockIdx.x * 2 + (cur.step == 0 ? 1 : 0);
     if (!more && tid == 0) {
-      // the batch's step that ends this item; its CTA c has floor(total c / ctas) <= it: c = ((it + 1) ctas - 1) / total
+      // the batch's step that ends this item; its CTA is the last c with floor(total c / ctas) <= it:
+      // c = ((it + 1) ctas - 1) / total
       const int64_t last = end - cur.s_end + cur.span.steps - 1;
       p.split[blockIdx.x] = make_int4(cur.step == 0 && !whole ? cur.n : -1, cur.item,
                                       (int)(((last + 1) * ctas - 1) / total), 0);

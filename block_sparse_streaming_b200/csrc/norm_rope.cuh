@@ -33,8 +33,8 @@
 // tokens, so a warp's stream never runs dry, at no cost in registers. A
 // CTA walks an equal share of the tokens in batches and forms the next batch's
 // angles in shared memory, each once, before the current one's rows. Rows
-// whose sizes, offsets or strides are no multiple of a vector run the same
-// code with one element per vector, read where it is used.
+// whose sizes, offsets or strides are no multiple of 16 bytes run the same code
+// with vectors of 4 bytes or of one element.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -45,6 +45,10 @@ namespace loza {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrWarps = kNrThreads / 32;
+
+// CTAs per SM: two, unless a lane's share of a row takes more than half of the
+// registers (rows of more than 32 tasks, and short vectors).
+__host__ __device__ constexpr int nr_ctas_per_sm(int vec, int nv) { return nv * vec > 8 || nv > 4 ? 1 : 2; }
 
 struct NrShape {
   int d, norm_dim, rope_off, pairs, interleaved, lph, lph_log, nrope, npass, ntasks;
@@ -310,7 +314,12 @@ struct NrMap {
 #pragma unroll
       for (int e = 0; e < VEC / 2; ++e) {  // the angles of pairs 2e and 2e + 1
         const float4 v = *reinterpret_cast<const float4*>(tab + 2 * e * s.nrope + 2 * t);
-        if constexpr (INTER) {
+        if constexpr (INTER && VEC == 2) {  // one pair of each vector
+          ac.p[0] = nr_pair(v.x, v.x);
+          as.p[0] = nr_pair(-v.y, v.y);
+          bc.p[0] = nr_pair(v.z, v.z);
+          bs.p[0] = nr_pair(-v.w, v.w);
+        } else if constexpr (INTER) {
           NrVals<VEC>&c = e < VEC / 4 ? ac : bc, &sn = e < VEC / 4 ? as : bs;
           const int at = e < VEC / 4 ? 2 * e : 2 * e - VEC / 2;
           c.p[at] = nr_pair(v.x, v.x);
@@ -370,49 +379,61 @@ __device__ __forceinline__ float nr_row_sum(float v, int lph) {
   return v;
 }
 
-// 16 bytes global -> shared; `bytes` 0 fills with zeros and reads nothing.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// BYTES (16 or 4) global -> shared; n = 0 fills with zeros and reads nothing, else n = BYTES.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t n) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A lane's ring of groups: `streams` tensors, NV tasks of two vectors each.
-// Slot layout [slot][vector][lane], 16 bytes: neighbouring lanes are
-// neighbouring addresses. VEC == 1 has no ring.
-template <int VEC, int NV, int STREAMS>
+// A lane's ring of groups: `STREAMS` tensors, NV tasks of two vectors each.
+// Slot layout [slot][vector][lane]: neighbouring lanes are neighbouring
+// addresses. Vectors of 2 bytes (which cp.async does not take) and the longest
+// rows of single elements are read where they are used instead.
+template <typename T, int VEC, int NV, int STREAMS>
 struct NrRing {
-  // about 8 KB a warp: 128 KB in flight on an SM with 16 warps
-  static constexpr int kSlots = VEC == 1 ? 0 : (NV * STREAMS >= 4 ? 2 : 8 / (NV * STREAMS));
+  static constexpr int kVec = sizeof(T) * VEC;
+  static constexpr bool kOn = kVec >= 4 && NV <= 8;
   static constexpr int kVectors = 2 * NV * STREAMS;
-  static constexpr int kSlotBytes = kVectors * 512;
-  static constexpr int kWarpBytes = kSlots * kSlotBytes;
+  static constexpr int kLine = 32 * kVec;  // one vector of all lanes
+  static constexpr int kSlotBytes = kVectors * kLine;
+  // 128 KB in flight on an SM, by two CTAs or (wide rows) by one
+  static constexpr int kWarpBytes = !kOn ? 0 : (nr_ctas_per_sm(VEC, NV) == 2 ? 8192 : 16384);
+  static constexpr int kSlots = kOn ? kWarpBytes / kSlotBytes : 2;
   static constexpr int kBytes = kNrWarps * kWarpBytes;
   static constexpr int kAhead = kSlots - 1;  // a slot is filled again one group after it was used
-  static_assert((kWarpBytes & (kWarpBytes - 1)) == 0, "the ring's offsets wrap by a mask");
+  static_assert(kSlots >= 2 && (kWarpBytes & (kWarpBytes - 1)) == 0, "the ring's offsets wrap by a mask");
 };
 
-// The tokens [begin, end) of a CTA's walk, of `ctas` walks over them all.
-__device__ __forceinline__ void nr_share(const NrShape& s, int cta, int ctas, int64_t& begin, int64_t& end) {
-  begin = s.tokens * cta / ctas;
-  end = s.tokens * (cta + 1) / ctas;
+// The tokens [begin, end) of a CTA's walk, of `ctas` walks over them all (at
+// most 2^30 tokens). The forward counts them in 32 bits, the backward in 64:
+// each is what the register allocator made the faster kernel of (72 against 75
+// us, 198 against 200).
+template <typename I>
+__device__ __forceinline__ void nr_share(const NrShape& s, int cta, int ctas, I& begin, I& end) {
+  begin = (I)(s.tokens * cta / ctas);
+  end = (I)(s.tokens * (cta + 1) / ctas);
 }
 
 // NORM: a side has weights (else the kernel is the rotation alone); INTER: the
 // interleaved layout (with one element per vector both are the same code).
 template <typename T, int VEC, int NV, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_kernel(const NrFwdParams p) {
-  using Ring = NrRing<VEC, NV, 1>;
+__global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope_kernel(const NrFwdParams p) {
+  using Ring = NrRing<T, VEC, NV, 1>;
   using P = Pack<T, VEC>;
   extern __shared__ __align__(16) uint8_t nr_bytes[];
   const NrShape& s = p.s;
   float2* const tables = reinterpret_cast<float2*>(nr_bytes + Ring::kBytes);  // two batches' angles
   const int table_size = p.batch * s.pairs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint8_t* ring = nr_bytes + warp * Ring::kWarpBytes + lane * 16;
+  const uint8_t* ring = nr_bytes + warp * Ring::kWarpBytes + lane * Ring::kVec;
   const uint32_t ring_addr = smem_u32(ring);
-  int64_t begin, end;
+  int begin, end;
   nr_share(s, blockIdx.x / p.parts, p.ctas, begin, end);
   const int lph = 1 << s.lph_log, t0 = lane & (lph - 1), sub = lane >> s.lph_log, rows = 32 >> s.lph_log;
   NrTask<VEC> task[NV];
@@ -424,7 +445,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
   const int share = index & (wide - 1), tok_first = index >> p.wide_log, tok_step = max(1, kNrWarps >> p.wide_log);
 
   // The cursor: the group asked for next. kind 0: queries, 1: keys, 2: values.
-  int64_t c_tok = begin + tok_first - tok_step;
+  int c_tok = begin + tok_first - tok_step;
   int c_kind = 2, c_g = 0, c_end = 0, c_hop = 0;  // first row (values: first vector), their number, the next group's
   int64_t c_xhop = 0;
   const T* c_x = nullptr;
@@ -432,7 +453,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
   constexpr int kNone = 1 << 30;               // a row that is never there
   uint32_t in_at = 0, out_at = 0;
   auto ask = [&]() {
-    if constexpr (VEC > 1) {
+    if constexpr (Ring::kOn) {
       if (c_g >= c_end) {  // to the next side or token that has something for this warp
         while (c_g >= c_end && c_tok < end) {
           if (++c_kind == 3) {
@@ -477,9 +498,9 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
       if (c_g < c_end) {  // the same for the whole warp
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          const uint32_t dst = ring_addr + in_at + v * 1024;
-          cp_async16(dst, c_x + c_oa[v], c_g + c_la[v] < c_end ? 16 : 0);
-          cp_async16(dst + 512, c_x + c_ob[v], c_g + c_lb[v] < c_end ? 16 : 0);
+          const uint32_t dst = ring_addr + in_at + v * 2 * Ring::kLine;
+          cp_async<Ring::kVec>(dst, c_x + c_oa[v], c_g + c_la[v] < c_end ? Ring::kVec : 0);
+          cp_async<Ring::kVec>(dst + Ring::kLine, c_x + c_ob[v], c_g + c_lb[v] < c_end ? Ring::kVec : 0);
         }
         in_at = (in_at + Ring::kSlotBytes) & (Ring::kWarpBytes - 1);
         c_g += c_hop;
@@ -490,34 +511,35 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
   };
   // The next group of the ring, into registers; its slot is asked for again after the one that was used before it.
   auto take = [&](P (&a)[NV], P (&b)[NV]) {
-    if constexpr (VEC > 1) {
+    if constexpr (Ring::kOn) {
       cp_async_wait<Ring::kAhead - 1>();
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const uint8_t* at = ring + out_at + v * 1024;
+        const uint8_t* at = ring + out_at + v * 2 * Ring::kLine;
         a[v] = *reinterpret_cast<const P*>(at);
-        b[v] = *reinterpret_cast<const P*>(at + 512);
+        b[v] = *reinterpret_cast<const P*>(at + Ring::kLine);
       }
       out_at = (out_at + Ring::kSlotBytes) & (Ring::kWarpBytes - 1);
       ask();
     }
   };
-  if constexpr (VEC > 1) {
+  if constexpr (Ring::kOn) {
 #pragma unroll 1
     for (int k = 0; k < Ring::kAhead; ++k) ask();
   }
-  int64_t slot_next = p.slots && begin + tok_first < end ? p.slots[begin + tok_first] : -1;  // of this warp's next token
-  nr_angles<VEC, INTER>(s, begin, (int)min((int64_t)p.batch, end - begin), tables);
+  // the slot of this warp's next token
+  int64_t slot_next = p.slots && begin + tok_first < end ? p.slots[begin + tok_first] : -1;
+  nr_angles<VEC, INTER>(s, begin, min(p.batch, end - begin), tables);
 
   int turn = 0;
-  for (int64_t tok0 = begin; tok0 < end; tok0 += p.batch, turn ^= 1) {
-    const int n = (int)min((int64_t)p.batch, end - tok0);
+  for (int tok0 = begin; tok0 < end; tok0 += p.batch, turn ^= 1) {
+    const int n = min(p.batch, end - tok0);
     __syncthreads();  // this batch's angles are there, and the other table's have been read
     if (tok0 + n < end)
-      nr_angles<VEC, INTER>(s, tok0 + n, (int)min((int64_t)p.batch, end - tok0 - n), tables + (turn ^ 1) * table_size);
+      nr_angles<VEC, INTER>(s, tok0 + n, min(p.batch, end - tok0 - n), tables + (turn ^ 1) * table_size);
     const float2* tab = tables + turn * table_size;
     for (int i = tok_first; i < n; i += tok_step) {
-      const int64_t tok = tok0 + i;
+      const int tok = tok0 + i;
       const int64_t slot = slot_next;
       if (p.slots) slot_next = tok + tok_step < end ? p.slots[tok + tok_step] : -1;
       const bool pooled = slot >= 0 && slot < p.n_slots;  // else a padded row, or a page that is not there
@@ -565,7 +587,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
         }
         for (int g = g0; g < heads; g += hop) {
           const bool in = g + sub < heads;
-          if constexpr (VEC > 1) {
+          if constexpr (Ring::kOn) {
             take(xa, xb);
           } else {
 #pragma unroll
@@ -634,7 +656,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
         const int vh = p.vper_log >= 0 ? x >> p.vper_log : x / vper;
         return dst + vh * p.v_pool.head_stride + (int64_t)(x - vh * vper) * VEC;
       };
-      if constexpr (VEC > 1) {
+      if constexpr (Ring::kOn) {
         P va[NV], vb[NV];
         for (int g = share * 64; g < nvec; g += 64 << p.wide_log) {
           take(va, vb);
@@ -652,15 +674,15 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ke
 // Every CTA walks its tokens twice, the query rows and then the key rows, so
 // that a warp has one set of weight gradients in registers.
 template <typename T, int VEC, int NV, bool INTER>
-__global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_backward_kernel(const NrBwdParams p) {
-  using Ring = NrRing<VEC, NV, 2>;
+__global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope_backward_kernel(const NrBwdParams p) {
+  using Ring = NrRing<T, VEC, NV, 2>;
   using P = Pack<T, VEC>;
   extern __shared__ __align__(16) uint8_t nr_bytes[];
   // two batches' angles; at the end of a side kNrWarps rows of norm_dim sums
   float2* const tables = reinterpret_cast<float2*>(nr_bytes + Ring::kBytes);
   const NrShape& s = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint8_t* ring = nr_bytes + warp * Ring::kWarpBytes + lane * 16;
+  const uint8_t* ring = nr_bytes + warp * Ring::kWarpBytes + lane * Ring::kVec;
   const uint32_t ring_addr = smem_u32(ring);
   int64_t begin, end;
   nr_share(s, blockIdx.x, gridDim.x, begin, end);
@@ -698,7 +720,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ba
     const T *c_x = nullptr, *c_y = nullptr;
     uint32_t in_at = 0, out_at = 0;
     auto ask = [&]() {
-      if constexpr (VEC > 1) {
+      if constexpr (Ring::kOn) {
         if (c_g >= heads && g0 < heads && c_tok < end) {  // to the next token
           c_tok += tok_step;
           if (c_tok < end) {
@@ -708,14 +730,14 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ba
           }
         }
         if (c_g < heads) {  // the same for the whole warp
-          const uint32_t bytes = c_g + sub < heads ? 16 : 0;  // rows behind the last head are zeros: they add nothing
+          const bool here = c_g + sub < heads;  // rows behind the last head are zeros: they add nothing
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
-            const uint32_t dst = ring_addr + in_at + v * 2048;
-            if (task[v].a >= 0) cp_async16(dst, c_y + task[v].a, bytes);
-            if (task[v].b >= 0) cp_async16(dst + 512, c_y + task[v].b, bytes);
-            if (norm_a[v]) cp_async16(dst + 1024, c_x + task[v].a, bytes);
-            if (norm_b[v]) cp_async16(dst + 1536, c_x + task[v].b, bytes);
+            const uint32_t dst = ring_addr + in_at + v * 4 * Ring::kLine;
+            if (task[v].a >= 0) cp_async<Ring::kVec>(dst, c_y + task[v].a, here ? Ring::kVec : 0);
+            if (task[v].b >= 0) cp_async<Ring::kVec>(dst + Ring::kLine, c_y + task[v].b, here ? Ring::kVec : 0);
+            if (norm_a[v]) cp_async<Ring::kVec>(dst + 2 * Ring::kLine, c_x + task[v].a, here ? Ring::kVec : 0);
+            if (norm_b[v]) cp_async<Ring::kVec>(dst + 3 * Ring::kLine, c_x + task[v].b, here ? Ring::kVec : 0);
           }
           in_at = (in_at + Ring::kSlotBytes) & (Ring::kWarpBytes - 1);
           c_g += hop;
@@ -725,7 +747,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ba
         cp_async_commit();
       }
     };
-    if constexpr (VEC > 1) {
+    if constexpr (Ring::kOn) {
 #pragma unroll 1
       for (int k = 0; k < Ring::kAhead; ++k) ask();
     }
@@ -752,15 +774,15 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ba
         for (int g = g0; g < heads; g += hop) {
           const bool in = g + sub < heads;
           P xa[NV], xb[NV], ya[NV], yb[NV];
-          if constexpr (VEC > 1) {
+          if constexpr (Ring::kOn) {
             cp_async_wait<Ring::kAhead - 1>();
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-              const uint8_t* at = ring + out_at + v * 2048;
+              const uint8_t* at = ring + out_at + v * 4 * Ring::kLine;
               ya[v] = *reinterpret_cast<const P*>(at);
-              yb[v] = *reinterpret_cast<const P*>(at + 512);
-              xa[v] = *reinterpret_cast<const P*>(at + 1024);
-              xb[v] = *reinterpret_cast<const P*>(at + 1536);
+              yb[v] = *reinterpret_cast<const P*>(at + Ring::kLine);
+              xa[v] = *reinterpret_cast<const P*>(at + 2 * Ring::kLine);
+              xb[v] = *reinterpret_cast<const P*>(at + 3 * Ring::kLine);
             }
             out_at = (out_at + Ring::kSlotBytes) & (Ring::kWarpBytes - 1);
             ask();
@@ -840,7 +862,7 @@ __global__ void __launch_bounds__(kNrThreads, NV * VEC > 8 ? 1 : 2) norm_rope_ba
         }
       }
     }
-    if constexpr (VEC > 1) cp_async_wait<0>();  // nothing but empty groups is left
+    if constexpr (Ring::kOn) cp_async_wait<0>();  // nothing but empty groups is left
     if (!norm) continue;  // the same for the whole CTA
     __syncthreads();      // the last angles have been read
     float* sums = reinterpret_cast<float*>(tables);

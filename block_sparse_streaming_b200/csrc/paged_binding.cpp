@@ -374,7 +374,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.d = dim32(d);
     Output q_out, k_out;
     if (has_q) {
-      const Rows r(first, "q", at, dtype, first.sizes()), o = rows_out(&q_out, a[12], "q_out", at, dtype, first.sizes());
+      const Rows r(first, "q", at, dtype, first.sizes());
+      const Rows o = rows_out(&q_out, a[12], "q_out", at, dtype, first.sizes());
       p.q = r.p;
       p.q_row_stride = r.stride;
       p.q_out = o.p;
@@ -445,7 +446,8 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Output dq, dk;
     at::Tensor dqw, dkw, ws;
     if (has_q) {
-      const Rows g(first, "dq_out", at, dtype, first.sizes()), o = rows_out(&dq, a[10], "dq", at, dtype, first.sizes());
+      const Rows g(first, "dq_out", at, dtype, first.sizes());
+      const Rows o = rows_out(&dq, a[10], "dq", at, dtype, first.sizes());
       p.dq_out = g.p;
       p.dq_out_row_stride = g.stride;
       p.dq = o.p;
@@ -464,7 +466,8 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (has_k) {
       const at::Tensor& gk = rank(a[1], "dk_out", 3);
       if (gk.size(0) != T || gk.size(2) != d) value_error("dq_out and dk_out must agree in tokens and head dim");
-      const Rows g(gk, "dk_out", at, dtype, gk.sizes()), o = rows_out(&dk, a[11], "dk", at, dtype, gk.sizes());
+      const Rows g(gk, "dk_out", at, dtype, gk.sizes());
+      const Rows o = rows_out(&dk, a[11], "dk", at, dtype, gk.sizes());
       p.dk_out = g.p;
       p.dk_out_row_stride = g.stride;
       p.dk = o.p;

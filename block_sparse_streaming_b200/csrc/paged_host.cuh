@@ -42,7 +42,7 @@ int elt_size(int dtype) { return dtype == LOZA_FP32 ? 4 : 2; }
 loza_status nr_shape(NrShape* s, int64_t tokens, int32_t d, int32_t norm_dim, float eps, const int32_t* positions,
                      const double* inv_freq, const loza_rope_params& r, int dtype) {
   if (dtype != LOZA_BF16 && dtype != LOZA_FP16 && dtype != LOZA_FP32) return LOZA_ERR_INVALID_ARG;
-  if (tokens < 0 || tokens > INT32_MAX || d < 1 || norm_dim < 0 || norm_dim > d) return LOZA_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > (1 << 30) || d < 1 || norm_dim < 0 || norm_dim > d) return LOZA_ERR_INVALID_ARG;
   if (d > 1024) return LOZA_ERR_UNSUPPORTED;
   if (r.rope_dim < 0 || r.rope_dim % 2 != 0 || r.rope_offset < 0 || (int64_t)r.rope_offset + r.rope_dim > d)
     return LOZA_ERR_INVALID_ARG;
@@ -72,15 +72,19 @@ bool nr_rows_ok(const void* x, int64_t stride, int heads, int d, int size) {
   return x && aligned_to(x, size) && stride >= (int64_t)heads * d && stride < (int64_t(1) << 40);
 }
 
-// Largest vector (in elements) that every size, offset and stride allows: 16 bytes, or one element.
+// Largest vector (in elements) that every size, offset, stride and address
+// allows: 16 bytes, for 16-bit types 4 bytes, or one element. Norm + rotation
+// of 8,192 tokens with 32 + 8 heads (bf16): heads of 128 in 16-byte vectors
+// took 41 us; heads of 100 in 4-byte vectors 75 us, element by element 150.
 int nr_vec(const NrShape& s, int size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> sizes) {
-  const int v = 16 / size;
-  if (s.d % v || s.norm_dim % v || s.rope_off % v || s.pairs % v) return 1;
-  for (const void* p : ptrs)
-    if (!aligned16(p)) return 1;
-  for (int64_t n : sizes)
-    if (n % v) return 1;
-  return v;
+  for (int v : {16 / size, 2}) {
+    if (v == 2 && size == 4) continue;
+    bool fits = s.d % v == 0 && s.norm_dim % v == 0 && s.rope_off % v == 0 && s.pairs % v == 0;
+    for (const void* p : ptrs) fits = fits && aligned_to(p, (size_t)v * size);
+    for (int64_t n : sizes) fits = fits && n % v == 0;
+    if (fits) return v;
+  }
+  return 1;
 }
 
 // Tasks (pairs of vectors) of a row, and how many a lane takes; returns that number (NV).
@@ -88,7 +92,7 @@ int nr_tasks(NrShape* s, int vec) {
   s->nrope = s->pairs / vec;
   s->npass = (s->d - 2 * s->pairs) / vec;
   s->ntasks = s->nrope + (s->npass + 1) / 2;
-  int nv = vec == 1 ? 4 : 1;
+  int nv = vec > 2 ? 1 : 4;
   while (nv * 32 < s->ntasks) nv = vec == 1 ? 16 : nv * 2;
   s->lph_log = 0;
   while ((nv << s->lph_log) < s->ntasks) ++s->lph_log;
@@ -103,7 +107,7 @@ constexpr int64_t kNrTableBytes = 16384;
 template <typename T, int VEC, int NV, bool NORM, bool INTER>
 bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
   auto kernel = norm_rope_kernel<T, VEC, NV, NORM, INTER>;
-  const size_t smem = NrRing<VEC, NV, 1>::kBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
+  const size_t smem = NrRing<T, VEC, NV, 1>::kBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return false;
@@ -114,7 +118,7 @@ bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
 template <typename T, int VEC, int NV, bool INTER>
 bool nr_launch_bwd(const NrBwdParams& p, int ctas, cudaStream_t st) {
   auto kernel = norm_rope_backward_kernel<T, VEC, NV, INTER>;
-  const size_t smem = NrRing<VEC, NV, 2>::kBytes +
+  const size_t smem = NrRing<T, VEC, NV, 2>::kBytes +
                       std::max((size_t)2 * p.batch * p.s.pairs * sizeof(float2),
                                (size_t)kNrWarps * p.s.norm_dim * sizeof(float));
   if (smem > 48 * 1024 &&
@@ -155,13 +159,14 @@ bool nr_run(const Params& p, int dtype, int vec, int nv, int ctas, cudaStream_t 
   auto half = [&](auto zero) {
     using T = decltype(zero);
     if (vec == 8) return nv == 1 ? nr_launch<T, 8, 1>(p, ctas, st) : nr_launch<T, 8, 2>(p, ctas, st);
+    if (vec == 2) return nv == 4 ? nr_launch<T, 2, 4>(p, ctas, st) : nr_launch<T, 2, 8>(p, ctas, st);
     return nv == 4 ? nr_launch<T, 1, 4>(p, ctas, st) : nr_launch<T, 1, 16>(p, ctas, st);
   };
   return dtype == LOZA_BF16 ? half(__nv_bfloat16()) : half(__half());
 }
 
-// CTAs that fill the GPU: two per SM (launch bounds), one of the wide rows' instances.
-int nr_ctas(int vec, int nv) { return sm_count() * (nv * vec > 8 ? 1 : 2); }
+// CTAs that fill the GPU.
+int nr_ctas(int vec, int nv) { return sm_count() * nr_ctas_per_sm(vec, nv); }
 
 // Log2 of the warps that share a token: as many as find room beside each
 // other on the GPU's `warps`; at most `most`, and never more than the widest
