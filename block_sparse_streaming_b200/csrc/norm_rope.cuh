@@ -484,8 +484,8 @@ __global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope
 #pragma unroll
               for (int v = 0; v < NV; ++v) {
                 const bool on = task[v].rot || !sd.skip_pass;
-                c_oa[v] = task[v].a;
-                c_ob[v] = task[v].b;
+                c_oa[v] = max(task[v].a, 0);  // no task: an aligned address that is not read
+                c_ob[v] = max(task[v].b, 0);
                 c_la[v] = on && task[v].a >= 0 ? sub : kNone;
                 c_lb[v] = on && task[v].b >= 0 ? sub : kNone;
               }

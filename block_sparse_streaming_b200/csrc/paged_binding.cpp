@@ -5,8 +5,9 @@
 // time; marshalling them in interpreted Python took longer than that (per call,
 // launch included, against here: rotation 11.5 / 5.4 us, norm + rotation into
 // pages 16 / 6.3, its gradient 27.5 / 11.4, page plan 15.5 / 8.8, decode 21 /
-// 8.9), so this part of the binding is compiled. No arithmetic on data happens here, and nothing is kept between
-// calls but the addresses of the C functions, which paged.py hands over.
+// 8.9), so this part of the binding is compiled. No arithmetic on data happens
+// here, and nothing is kept between calls but the addresses of the C functions,
+// which paged.py hands over.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -269,9 +270,15 @@ void expect(Py_ssize_t got, Py_ssize_t want) {
 
 PyObject* tuple(std::initializer_list<PyObject*> items) {
   PyObject* t = PyTuple_New((Py_ssize_t)items.size());
+  bool whole = t != nullptr;
   Py_ssize_t i = 0;
-  for (PyObject* o : items) PyTuple_SET_ITEM(t, i++, o);
-  return t;
+  for (PyObject* o : items) {
+    whole = whole && o;
+    if (t) PyTuple_SET_ITEM(t, i++, o); else Py_XDECREF(o);
+  }
+  if (whole) return t;
+  Py_XDECREF(t);
+  throw PythonError{};  // out of memory: already set
 }
 
 // (ctx_lens, new_lens, free_pages, block_table, page_size, capacity)

@@ -535,14 +535,16 @@ loza_status loza_rope_frequencies(double theta, int32_t rope_dim, int32_t scalin
 
 /*
  * Rotation of one tensor: out[t, h] = x[t, h] with the columns of `rope` turned
- * by positions[t]. x, out [tokens, n_heads, d] (d <= 1024), rows x_row_stride
- * and out_row_stride elements apart, heads contiguous within a row, dtype any
- * of the three; positions device int32 [tokens] (any value); inv_freq DEVICE
+ * by positions[t]. x, out [tokens, n_heads, d] (0 <= tokens <= 2^30, n_heads
+ * <= 65,535, d <= 1024), rows x_row_stride and out_row_stride elements apart (at
+ * least n_heads * d), heads contiguous within a row, dtype any of the three;
+ * positions device int32 [tokens] (any value, any order); inv_freq DEVICE
  * double [rope_dim / 2]. out may be x with the same stride (then only the
  * rotated columns are touched) or must not overlap it. transposed = 1 applies
  * the transposed map, which is the gradient: dx from dout. 32-bit arithmetic,
  * one rounding. Sizes, offsets, strides and pointers that are multiples of 16
- * bytes run in 16-byte vectors; others, element by element.
+ * bytes run in 16-byte vectors; others in vectors of 4 bytes or element by
+ * element.
  */
 typedef struct {
     const void *x;
@@ -562,7 +564,8 @@ loza_status loza_rope(const loza_rope_args *args, loza_stream_t stream);
  * n_kv_heads, d]:
  *     n_c = weight_c x_c / sqrt(mean(x_0 .. x_{norm_dim-1} squared) + eps)  for c < norm_dim
  *     n_c = x_c  for the other columns, and for a side whose weight is NULL
- * then the rotation of loza_rope; 32-bit arithmetic, one rounding.
+ * then the rotation of loza_rope; 32-bit arithmetic (squares above 3.4e38
+ * overflow), one rounding; eps >= 0; sizes as there.
  *   q, k, v   rows q_row_stride, k_row_stride, v_row_stride elements apart, so
  *             they may be slices of one projection's rows; n_heads or
  *             n_kv_heads may be 0 (that side's arguments are then not read)

@@ -302,6 +302,110 @@ def test_norm_rope_backward(bss, dtype, shape, T, H, Hk, interleaved):
     assert torch.equal(place[0], once[0]) and torch.equal(place[1], once[1])
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,dim,off,nd", [(8, 4, 2, 6), (66, 60, 4, 66), (128, 128, 0, 128), (514, 260, 10, 500),
+                                          (1022, 1020, 2, 1022)])
+def test_rows_of_four_byte_alignment(bss, dtype, interleaved, d, dim, off, nd):
+    """Head slices that begin two elements into their rows, and head dims that 16-byte vectors do not fit: rotation,
+    norm, cache write and gradient, all in place of slices of one buffer, whose other columns stay as they were."""
+    dt, T, H, Hk = DTYPES[dtype], 19, 3, 2
+    pos, freq, pos_d, freq_d = rope_inputs(bss, d, T, dim)
+    rope, eps = bss.RopeParams(dim, off, interleaved, 0.5), 1e-5
+    wide = (H + 2 * Hk) * d + 6
+    rows = normal(d, T, wide, dtype=dt)
+    cut = lambda r: (r[:, 2:2 + H * d].view(T, H, d), r[:, 4 + H * d:4 + (H + Hk) * d].view(T, Hk, d),
+                     r[:, 4 + (H + Hk) * d:4 + (H + 2 * Hk) * d].view(T, Hk, d))
+    q, k, v = cut(rows)
+    qw, kw = normal(1, nd + 2, dtype=dt)[2:] + 1, normal(2, nd, dtype=dt) + 1
+    want_r, size_r = paged.rotate(f64(q), pos, freq, off, interleaved, 0.5)
+    close(bss.loza_rope(q, pos_d, freq_d, rope), want_r, 12 * STEP * size_r, "rope 4-byte")
+    want = [paged.norm_rope(f64(x), f64(w), nd, float(np.float32(eps)), pos, freq, off, interleaved, 0.5)
+            for x, w in ((q, qw), (k, kw))]
+    back = [paged.norm_rope_backward(f64(x), f64(x), f64(w), nd, float(np.float32(eps)), pos, freq, off, interleaved,
+                                     0.5) for x, w in ((q, qw), (k, kw))]
+    grads = rows.clone()
+    gq, gk, _ = cut(grads)
+    _, _, dqw, dkw = bss.loza_qk_norm_rope_backward(gq, gk, q, k, pos_d, freq_d, rope, qw, kw, eps, dq=gq, dk=gk)
+    for dx, dw, (wx, sx, ww, sw), x in ((gq, dqw, back[0], q), (gk, dkw, back[1], k)):
+        close(dx, wx, 96 * STEP * sx, "bwd 4-byte")
+        close(dw, ww, (48 + T * x.shape[1]) * STEP * sw, "bwd weight 4-byte")
+    place = rows.clone()
+    pq, pk, pv = cut(place)
+    pool = torch.full((2, 2, 16, Hk, d), 5.0, dtype=dt, device="cuda")
+    slots = torch.arange(T, device="cuda") + 7
+    bss.loza_qk_norm_rope(pq, pk, pos_d, freq_d, rope, qw, kw, eps, v=pv, k_pool=pool[:, 0], v_pool=pool[:, 1],
+                          slots=slots, q_out=pq, k_out=pk)
+    for x, (wx, sx) in ((pq, want[0]), (pk, want[1])):
+        close(x, wx, norm_slack(None, nd, sx, d), "norm_rope 4-byte")
+    flat = [pool[:, i].reshape(32, Hk, d) for i in range(2)]
+    assert torch.equal(flat[0][slots], pk) and torch.equal(flat[1][slots], v)
+    rest = [i for i in range(32) if not 7 <= i < 7 + T]
+    assert (flat[0][rest] == 5).all() and (flat[1][rest] == 5).all()
+    for buf in (grads, place):  # between and beside the slices
+        for x, y in zip(cut(buf)[:2], (q, k)):
+            x.copy_(y)
+        assert torch.equal(buf, rows)
+
+
+def test_rows_far_apart(bss):
+    """Rows whose offsets pass 2^31 elements and 2^32 bytes, forward and backward."""
+    T, H, d, stride = 1100, 2, 64, 1 << 21
+    buf = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda").view(T, stride)
+    pos, freq, pos_d, freq_d = rope_inputs(bss, 4, T, d)
+    rope = bss.RopeParams(d)
+    x, dy = normal(1, T, H, d, dtype=torch.bfloat16), normal(2, T, H, d, dtype=torch.bfloat16)
+    w = normal(3, d, dtype=torch.bfloat16) + 1
+    cut = lambda i: buf[:, i * H * d:(i + 1) * H * d].view(T, H, d)
+    cut(0).copy_(x)
+    cut(1).copy_(dy)
+    bss.loza_rope(cut(0), pos_d, freq_d, rope, out=cut(2))
+    bss.loza_qk_norm_rope(cut(0), None, pos_d, freq_d, rope, w, q_out=cut(3))
+    far = bss.loza_qk_norm_rope_backward(cut(1), None, cut(0), None, pos_d, freq_d, rope, w, dq=cut(4))
+    near = bss.loza_qk_norm_rope_backward(dy, None, x, None, pos_d, freq_d, rope, w)
+    assert torch.equal(cut(2), bss.loza_rope(x, pos_d, freq_d, rope))
+    assert torch.equal(cut(3), bss.loza_qk_norm_rope(x, None, pos_d, freq_d, rope, w)[0])
+    assert torch.equal(cut(4), near[0]) and torch.equal(far[2], near[2])
+
+
+def test_captured_rotation_and_gradient_on_two_streams(bss):
+    """Rotation, norm and gradient captured on two streams with buffers of their own (the gradient's workspace, made
+    inside the capture, among them), replayed at the same time over new inputs: the bits of calls made one by one."""
+    T, H, Hk, d = 900, 8, 2, 128
+    pos, freq, pos_d, freq_d = rope_inputs(bss, 8, T, d)
+    rope = bss.RopeParams(d)
+    w = normal(1, d, dtype=torch.bfloat16) + 1
+    make = lambda s: [normal(s + i, T, n, d, dtype=torch.bfloat16) for i, n in enumerate((H, Hk, H, Hk))]
+
+    def run(q, k, gq, gk):
+        return (bss.loza_rope(q, pos_d, freq_d, rope, transposed=True), *bss.loza_qk_norm_rope(
+            q, k, pos_d, freq_d, rope, w, w), *bss.loza_qk_norm_rope_backward(gq, gk, q, k, pos_d, freq_d, rope, w, w))
+
+    runs = []
+    for i in range(2):
+        st, x = torch.cuda.Stream(), make(10 * i)
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            run(*x)
+        st.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            out = run(*x)
+        runs.append((st, g, x, out))
+    for seed in (100, 200):
+        for i, (_, _, x, _) in enumerate(runs):
+            for a, b in zip(x, make(seed + 10 * i)):
+                a.copy_(b)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for st, g, *_rest in runs:
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for _, _, x, out in runs:
+            assert all(torch.equal(a, b) for a, b in zip(out, run(*x)))
+
+
 def test_norm_rope_backward_of_no_tokens(bss):
     e = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")
     pos, freq, pos_d, freq_d = rope_inputs(bss, 1, 0, 64)
