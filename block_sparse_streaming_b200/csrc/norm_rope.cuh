@@ -31,7 +31,8 @@
 // every lane fills by cp.async for itself alone (it reads back what it asked
 // for: no barrier); a cursor asks ahead of the arithmetic across sides and
 // tokens, so a warp's stream never runs dry, at no cost in registers. A
-// CTA walks an equal share of the tokens in batches and forms the next batch's
+// CTA walks its tokens (an equal share, or a short walk of many that are dealt
+// out as CTAs end) in batches and forms the next batch's
 // angles in shared memory, each once, before the current one's rows. Rows
 // whose sizes, offsets or strides are no multiple of 16 bytes run the same code
 // with vectors of 4 bytes or of one element.
@@ -81,7 +82,8 @@ struct NrFwdParams {
   const int64_t* slots;
   int64_t n_slots;  // num_pages * page_size
   int page_shift, d_v;
-  int ctas;             // each walks an equal share of the tokens
+  int ctas;             // each walks `walk` tokens or, if that is 0, an equal share of them
+  int walk;
   int parts;            // CTAs that share one such walk (when there are few tokens)
   int batch;            // tokens per step of a walk
   int wide_log;         // log2 of the warps that share a token
@@ -434,7 +436,12 @@ __global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope
   const uint8_t* ring = nr_bytes + warp * Ring::kWarpBytes + lane * Ring::kVec;
   const uint32_t ring_addr = smem_u32(ring);
   int begin, end;
-  nr_share(s, blockIdx.x / p.parts, p.ctas, begin, end);
+  if (p.walk) {
+    begin = (int)(blockIdx.x / p.parts) * p.walk;
+    end = (int)min(s.tokens, (int64_t)begin + p.walk);
+  } else {
+    nr_share(s, blockIdx.x / p.parts, p.ctas, begin, end);
+  }
   const int lph = 1 << s.lph_log, t0 = lane & (lph - 1), sub = lane >> s.lph_log, rows = 32 >> s.lph_log;
   NrTask<VEC> task[NV];
 #pragma unroll

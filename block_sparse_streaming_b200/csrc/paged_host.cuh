@@ -188,15 +188,35 @@ int nr_batch(const NrShape& s, int wide_log) {
   return step * each;
 }
 
-// The forward's walk, from the groups of the widest side. With fewer tokens
-// than CTAs several CTAs share a token.
-void nr_plan_fwd(NrFwdParams* p, int vec, int nv, int64_t groups) {
+// The forward's walk, from the groups of the widest side and of a whole token.
+// With fewer tokens than CTAs several CTAs share a token. With many, equal
+// shares end up to 40 % apart: SMs do not get equal shares of the memory's
+// bandwidth (a pure copy's CTAs ended between 60 and 135 us). Short walks that
+// the hardware deals out as SMs become free even this out, but each starts with
+// an empty ring and angles to form. They pay where a warp's walk is long
+// enough: rotation of 16,411 tokens, 64 heads of 192 (32 groups) 151 -> 129 us;
+// 16,384 tokens, 32 + 8 heads of 128 into pages without weights (12 groups)
+// 77 -> 64, in fp32 with weights (24) 153 -> 128, 64 + 8 heads with weights (20)
+// 128 -> 115. Not below: with weights and 12 groups 73 -> 81, the rotation of 8
+// heads (2 groups) 65 -> 71, rows of 4-byte vectors 29 -> 33; nor with less
+// than one and a half walks per CTA (1.05: 15 -> 19).
+void nr_plan_fwd(NrFwdParams* p, int vec, int nv, int size, int64_t groups, int64_t token_groups) {
   const int64_t ctas = nr_ctas(vec, nv);
   p->wide_log = nr_wide(p->s.tokens, groups, ctas * kNrWarps, 64);
   p->parts = std::max(1, (1 << p->wide_log) / kNrWarps);
   const int64_t need = ((p->s.tokens << p->wide_log) + kNrWarps - 1) / kNrWarps;  // a token or more for every warp
   p->ctas = (int)std::max<int64_t>(1, std::min<int64_t>({p->s.tokens, ctas / p->parts, need}));
   p->batch = nr_batch(p->s, p->wide_log);
+  const bool norm = p->q.w || p->k.w;
+  if (vec * size == 16 && p->wide_log == 0 && token_groups >= (norm ? 16 : 8)) {
+    const int64_t least = norm ? 24 : 12;  // groups of a warp's walk
+    const int64_t walk = kNrWarps * ((least + token_groups - 1) / token_groups);
+    const int64_t walks = (p->s.tokens + walk - 1) / walk;
+    if (walks * 2 >= ctas * 3) {
+      p->walk = (int)walk;
+      p->ctas = (int)walks;
+    }
+  }
 }
 
 // CTAs of the backward at most (the workspace holds a row of sums per side for each).
@@ -364,7 +384,7 @@ loza_status loza_rope(const loza_rope_args* args, loza_stream_t stream) {
   }
   const int rows = 32 >> p.s.lph_log;
   const int64_t groups = (a.n_heads + rows - 1) / rows;
-  nr_plan_fwd(&p, vec, nv, groups);
+  nr_plan_fwd(&p, vec, nv, size, groups, groups);
   if (!nr_run(p, a.dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return LOZA_OK;
@@ -434,7 +454,8 @@ loza_status loza_qk_norm_rope(const loza_qk_norm_rope_args* args, loza_stream_t 
   const int rows = 32 >> p.s.lph_log;
   const int vper = p.d_v / vec;
   p.vper_log = vper > 0 && (vper & (vper - 1)) == 0 ? log2_of(vper) : -1;
-  nr_plan_fwd(&p, vec, nv, (std::max(a.n_heads, a.n_kv_heads) + rows - 1) / rows);
+  const int64_t gq = (a.n_heads + rows - 1) / rows, gk = (a.n_kv_heads + rows - 1) / rows;
+  nr_plan_fwd(&p, vec, nv, size, std::max(gq, gk), gq + gk + ((int64_t)a.n_kv_heads * vper + 63) / 64);
   if (!nr_run(p, a.dtype, vec, nv, 0, reinterpret_cast<cudaStream_t>(stream))) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return LOZA_OK;

@@ -368,6 +368,39 @@ def test_rows_far_apart(bss):
     assert torch.equal(cut(4), near[0]) and torch.equal(far[2], near[2])
 
 
+@pytest.mark.parametrize("dtype,H,Hk,d,weights,T", [
+    ("bf16", 32, 0, 128, False, 7201), ("bf16", 32, 8, 128, False, 3601), ("fp32", 32, 8, 128, True, 3555),
+    ("bf16", 64, 8, 128, True, 7150), ("fp16", 24, 1, 576, True, 3003), ("bf16", 8, 8, 64, True, 5003)])
+def test_tokens_are_dealt_in_any_way(bss, dtype, H, Hk, d, weights, T):
+    """Many tokens (equal shares, or short walks dealt out one after another) give the bits of the same tokens a few
+    at a time, which the tests above compare with the oracle; rows behind the last token stay as they were."""
+    dt = DTYPES[dtype]
+    pos, freq, pos_d, freq_d = rope_inputs(bss, 9, T, 64)
+    rope = bss.RopeParams(64, d - 64, True)
+    q = normal(1, T, H, d, dtype=dt)
+    k, v = (normal(s, T, Hk, d, dtype=dt) for s in (2, 3)) if Hk else (None, None)
+    w = normal(4, d, dtype=dt) + 1 if weights else None
+    slots = torch.randperm(T + 20, generator=torch.Generator().manual_seed(5)).cuda()[:T]
+
+    def run(a, b, q_out, k_pool, v_pool):
+        if not Hk:
+            return bss.loza_rope(q[a:b], pos_d[a:b], freq_d, rope, out=q_out[a:b])
+        bss.loza_qk_norm_rope(q[a:b], k[a:b], pos_d[a:b], freq_d, rope, w, w, v=v[a:b], k_pool=k_pool, v_pool=v_pool,
+                              slots=slots[a:b], q_out=q_out[a:b])
+
+    def fresh():
+        pages = -(-(T + 20) // 16)
+        return (torch.full((T + 8, H, d), 3.0, dtype=dt, device="cuda"),
+                *(torch.full((pages, 16, max(Hk, 1), d), 4.0, dtype=dt, device="cuda") for _ in range(2)))
+
+    once, parts = fresh(), fresh()
+    run(0, T, *once)
+    for a in range(0, T, 400):
+        run(a, min(a + 400, T), *parts)
+    assert all(torch.equal(x, y) for x, y in zip(once, parts))
+    assert (once[0][T:] == 3).all()
+
+
 def test_captured_rotation_and_gradient_on_two_streams(bss):
     """Rotation, norm and gradient captured on two streams with buffers of their own (the gradient's workspace, made
     inside the capture, among them), replayed at the same time over new inputs: the bits of calls made one by one."""
