@@ -31,11 +31,12 @@
 // every lane fills by cp.async for itself alone (it reads back what it asked
 // for: no barrier); a cursor asks ahead of the arithmetic across sides and
 // tokens, so a warp's stream never runs dry, at no cost in registers. A
-// CTA walks its tokens (an equal share, or a short walk of many that are dealt
-// out as CTAs end) in batches and forms the next batch's
-// angles in shared memory, each once, before the current one's rows. Rows
-// whose sizes, offsets or strides are no multiple of 16 bytes run the same code
-// with vectors of 4 bytes or of one element.
+// forward warp, alone in its CTA, walks its tokens (an equal share, or a short
+// walk of many that are dealt out as warps end: see nr_plan_fwd), a CTA of the
+// gradient an equal share, in batches; the next batch's angles are formed in
+// shared memory, each once, before the current one's rows. Rows whose sizes,
+// offsets or strides are no multiple of 16 bytes run the same code with vectors
+// of 4 bytes or of one element.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -47,13 +48,17 @@ namespace loza {
 constexpr int kNrThreads = 256;
 constexpr int kNrWarps = kNrThreads / 32;
 
-// CTAs per SM: two, unless a lane's share of a row takes more than half of the
-// registers (rows of more than 32 tasks, and short vectors).
-__host__ __device__ constexpr int nr_ctas_per_sm(int vec, int nv) { return nv * vec > 8 || nv > 4 ? 1 : 2; }
+// Warps per SM: 16, unless a lane's share of a row takes more than half of the
+// registers (rows of more than 32 tasks, and short vectors). The forward's CTAs
+// are single warps: none waits for another at a barrier or at its end (CTAs of
+// 8 warps: rotation of 64 x 64 heads of 576 5.3 against 4.8 us, norm of 8,192
+// tokens with 64 + 64 heads of 192 212 against 198). The gradient's have 8, to
+// sum the weights' gradients over.
+__host__ __device__ constexpr int nr_warps_per_sm(int vec, int nv) { return nv * vec > 8 || nv > 4 ? 8 : 16; }
+__host__ __device__ constexpr int nr_ctas_per_sm(int vec, int nv) { return nr_warps_per_sm(vec, nv) / kNrWarps; }
 
 struct NrShape {
   int d, norm_dim, rope_off, pairs, interleaved, lph, lph_log, nrope, npass, ntasks;
-  int per;           // tokens whose angles a CTA forms at a time
   float scale, sign, eps, inv_norm;  // sign -1: the transposed rotation
   const double* inv_freq;
   const int32_t* positions;
@@ -82,11 +87,10 @@ struct NrFwdParams {
   const int64_t* slots;
   int64_t n_slots;  // num_pages * page_size
   int page_shift, d_v;
-  int ctas;             // each walks `walk` tokens or, if that is 0, an equal share of them
+  int walks;            // of `walk` tokens each or, if that is 0, equal shares of them
   int walk;
-  int parts;            // CTAs that share one such walk (when there are few tokens)
   int batch;            // tokens per step of a walk
-  int wide_log;         // log2 of the warps that share a token
+  int wide_log;         // log2 of the warps (CTAs) that share a walk, when there are few tokens
   int vper_log;         // log2 of the vectors per value row, or -1
 };
 
@@ -154,17 +158,17 @@ struct NrTask {
   }
 };
 
-// cos and sin (times scale and sign) of the angles of tokens [tok0, tok0 + n), by the whole CTA. Within a token,
+// cos and sin (times scale and sign) of the angles of tokens [tok0, tok0 + n), by the CTA's threads. Within a token,
 // the VEC angles of task t are laid out so that the lanes of a row read consecutive 16 bytes: angle e is at
 // (e / 2) (2 nrope) + 2 t + e % 2. They are those of pairs t VEC + e or, interleaved, of the VEC / 2 pairs of the
 // task's first vector and the VEC / 2 of its second one, half the rotated columns on.
-template <int VEC, bool INTER>
+template <int VEC, bool INTER, int THREADS>
 __device__ __forceinline__ void nr_angles(const NrShape& s, int64_t tok0, int n, float2* tab) {
   if (s.pairs == 0) return;
   // a thread keeps its pair (or few pairs) and walks the tokens, `per` of them at a time
-  const int per = s.per, i0 = s.pairs < kNrThreads ? threadIdx.x / s.pairs : 0;
+  const int per = max(1, THREADS / s.pairs), i0 = s.pairs < THREADS ? threadIdx.x / s.pairs : 0;
   if (i0 >= per) return;
-  for (int pair = threadIdx.x - i0 * s.pairs; pair < s.pairs; pair += kNrThreads) {
+  for (int pair = threadIdx.x - i0 * s.pairs; pair < s.pairs; pair += THREADS) {
     const double freq = s.inv_freq[pair] * 0.15915494309189533577;  // turns: 1 / (2 pi)
     int t = pair / VEC, e = pair - t * VEC;
     if constexpr (INTER && VEC > 1) {
@@ -180,7 +184,7 @@ __device__ __forceinline__ void nr_angles(const NrShape& s, int64_t tok0, int n,
       sincospif(2.f * (float)turns, &sn, &cs);
       tab[i * s.pairs + at] = make_float2(cs * s.scale, sn * s.scale * s.sign);
     }
-    if (s.pairs < kNrThreads) break;
+    if (s.pairs < THREADS) break;
   }
 }
 
@@ -404,55 +408,52 @@ struct NrRing {
   static constexpr int kVectors = 2 * NV * STREAMS;
   static constexpr int kLine = 32 * kVec;  // one vector of all lanes
   static constexpr int kSlotBytes = kVectors * kLine;
-  // 128 KB in flight on an SM, by two CTAs or (wide rows) by one
-  static constexpr int kWarpBytes = !kOn ? 0 : (nr_ctas_per_sm(VEC, NV) == 2 ? 8192 : 16384);
+  // 128 KB in flight on an SM
+  static constexpr int kWarpBytes = !kOn ? 0 : 131072 / nr_warps_per_sm(VEC, NV);
   static constexpr int kSlots = kOn ? kWarpBytes / kSlotBytes : 2;
-  static constexpr int kBytes = kNrWarps * kWarpBytes;
   static constexpr int kAhead = kSlots - 1;  // a slot is filled again one group after it was used
   static_assert(kSlots >= 2 && (kWarpBytes & (kWarpBytes - 1)) == 0, "the ring's offsets wrap by a mask");
 };
 
-// The tokens [begin, end) of a CTA's walk, of `ctas` walks over them all (at
+// The tokens [begin, end) of a walk, of `walks` equal ones over them all (at
 // most 2^30 tokens). The forward counts them in 32 bits, the backward in 64:
 // each is what the register allocator made the faster kernel of (72 against 75
 // us, 198 against 200).
 template <typename I>
-__device__ __forceinline__ void nr_share(const NrShape& s, int cta, int ctas, I& begin, I& end) {
-  begin = (I)(s.tokens * cta / ctas);
-  end = (I)(s.tokens * (cta + 1) / ctas);
+__device__ __forceinline__ void nr_share(const NrShape& s, int walk, int walks, I& begin, I& end) {
+  begin = (I)(s.tokens * walk / walks);
+  end = (I)(s.tokens * (walk + 1) / walks);
 }
 
 // NORM: a side has weights (else the kernel is the rotation alone); INTER: the
 // interleaved layout (with one element per vector both are the same code).
 template <typename T, int VEC, int NV, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope_kernel(const NrFwdParams p) {
+__global__ void __launch_bounds__(32, nr_warps_per_sm(VEC, NV)) norm_rope_kernel(const NrFwdParams p) {
   using Ring = NrRing<T, VEC, NV, 1>;
   using P = Pack<T, VEC>;
   extern __shared__ __align__(16) uint8_t nr_bytes[];
   const NrShape& s = p.s;
-  float2* const tables = reinterpret_cast<float2*>(nr_bytes + Ring::kBytes);  // two batches' angles
+  float2* const tables = reinterpret_cast<float2*>(nr_bytes + Ring::kWarpBytes);  // two batches' angles
   const int table_size = p.batch * s.pairs;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint8_t* ring = nr_bytes + warp * Ring::kWarpBytes + lane * Ring::kVec;
+  const int lane = threadIdx.x;
+  const uint8_t* ring = nr_bytes + lane * Ring::kVec;
   const uint32_t ring_addr = smem_u32(ring);
   int begin, end;
   if (p.walk) {
-    begin = (int)(blockIdx.x / p.parts) * p.walk;
+    begin = (int)blockIdx.x * p.walk;
     end = (int)min(s.tokens, (int64_t)begin + p.walk);
   } else {
-    nr_share(s, blockIdx.x / p.parts, p.ctas, begin, end);
+    nr_share(s, blockIdx.x >> p.wide_log, p.walks, begin, end);
   }
   const int lph = 1 << s.lph_log, t0 = lane & (lph - 1), sub = lane >> s.lph_log, rows = 32 >> s.lph_log;
   NrTask<VEC> task[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) task[v] = NrTask<VEC>(s, t0 + v * lph);
   const int vper = p.d_v / VEC, nvec = p.k.heads * vper;
-  // this warp's tokens (from tok_first in steps) and its share of their groups
-  const int index = (blockIdx.x % p.parts) * kNrWarps + warp, wide = 1 << p.wide_log;
-  const int share = index & (wide - 1), tok_first = index >> p.wide_log, tok_step = max(1, kNrWarps >> p.wide_log);
+  const int share = blockIdx.x & ((1 << p.wide_log) - 1);  // of a token's groups
 
   // The cursor: the group asked for next. kind 0: queries, 1: keys, 2: values.
-  int c_tok = begin + tok_first - tok_step;
+  int c_tok = begin - 1;
   int c_kind = 2, c_g = 0, c_end = 0, c_hop = 0;  // first row (values: first vector), their number, the next group's
   int64_t c_xhop = 0;
   const T* c_x = nullptr;
@@ -465,8 +466,7 @@ __global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope
         while (c_g >= c_end && c_tok < end) {
           if (++c_kind == 3) {
             c_kind = 0;
-            c_tok += tok_step;
-            if (c_tok >= end) break;
+            if (++c_tok >= end) break;
           }
           if (c_kind == 2) {
             c_g = share * 64;
@@ -534,21 +534,20 @@ __global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope
 #pragma unroll 1
     for (int k = 0; k < Ring::kAhead; ++k) ask();
   }
-  // the slot of this warp's next token
-  int64_t slot_next = p.slots && begin + tok_first < end ? p.slots[begin + tok_first] : -1;
-  nr_angles<VEC, INTER>(s, begin, min(p.batch, end - begin), tables);
+  int64_t slot_next = p.slots && begin < end ? p.slots[begin] : -1;  // the next token's
+  nr_angles<VEC, INTER, 32>(s, begin, min(p.batch, end - begin), tables);
 
   int turn = 0;
   for (int tok0 = begin; tok0 < end; tok0 += p.batch, turn ^= 1) {
     const int n = min(p.batch, end - tok0);
-    __syncthreads();  // this batch's angles are there, and the other table's have been read
+    __syncwarp();  // this batch's angles are there, and the other table's have been read
     if (tok0 + n < end)
-      nr_angles<VEC, INTER>(s, tok0 + n, min(p.batch, end - tok0 - n), tables + (turn ^ 1) * table_size);
+      nr_angles<VEC, INTER, 32>(s, tok0 + n, min(p.batch, end - tok0 - n), tables + (turn ^ 1) * table_size);
     const float2* tab = tables + turn * table_size;
-    for (int i = tok_first; i < n; i += tok_step) {
+    for (int i = 0; i < n; ++i) {
       const int tok = tok0 + i;
       const int64_t slot = slot_next;
-      if (p.slots) slot_next = tok + tok_step < end ? p.slots[tok + tok_step] : -1;
+      if (p.slots) slot_next = tok + 1 < end ? p.slots[tok + 1] : -1;
       const bool pooled = slot >= 0 && slot < p.n_slots;  // else a padded row, or a page that is not there
       const int64_t page = slot >> p.page_shift, prow = slot & ((1 << p.page_shift) - 1);
 #pragma unroll
@@ -686,7 +685,7 @@ __global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope
   using P = Pack<T, VEC>;
   extern __shared__ __align__(16) uint8_t nr_bytes[];
   // two batches' angles; at the end of a side kNrWarps rows of norm_dim sums
-  float2* const tables = reinterpret_cast<float2*>(nr_bytes + Ring::kBytes);
+  float2* const tables = reinterpret_cast<float2*>(nr_bytes + kNrWarps * Ring::kWarpBytes);
   const NrShape& s = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint8_t* ring = nr_bytes + warp * Ring::kWarpBytes + lane * Ring::kVec;
@@ -759,14 +758,14 @@ __global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope
       for (int k = 0; k < Ring::kAhead; ++k) ask();
     }
     __syncthreads();  // the other side's sums have been read
-    nr_angles<VEC, INTER>(s, begin, (int)min((int64_t)batch, end - begin), tables);
+    nr_angles<VEC, INTER, kNrThreads>(s, begin, (int)min((int64_t)batch, end - begin), tables);
 
     int turn = 0;
     for (int64_t tok0 = begin; tok0 < end; tok0 += batch, turn ^= 1) {
       const int n = (int)min((int64_t)batch, end - tok0);
       __syncthreads();  // this batch's angles are there, and the other table's have been read
       if (tok0 + n < end)
-        nr_angles<VEC, INTER>(s, tok0 + n, (int)min((int64_t)batch, end - tok0 - n), tables + (turn ^ 1) * table_size);
+        nr_angles<VEC, INTER, kNrThreads>(s, tok0 + n, (int)min((int64_t)batch, end - tok0 - n), tables + (turn ^ 1) * table_size);
       const float2* tab = tables + turn * table_size;
       for (int i = tok_first; i < n; i += tok_step) {
         const int h = g0 + sub;

@@ -56,7 +56,6 @@ loza_status nr_shape(NrShape* s, int64_t tokens, int32_t d, int32_t norm_dim, fl
   s->norm_dim = norm_dim;
   s->rope_off = r.rope_offset;
   s->pairs = r.rope_dim / 2;
-  s->per = s->pairs > 0 ? std::max(1, kNrThreads / s->pairs) : 1;
   s->interleaved = r.interleaved;
   s->scale = r.scale;
   s->sign = 1.f;
@@ -100,25 +99,25 @@ int nr_tasks(NrShape* s, int vec) {
   return nv;
 }
 
-// Angles of a batch: 16 KB lets two CTAs and their rings share an SM; one token per warp of the longest table (512
-// pairs, 32 KB) always fits, on an SM of its own (rows that long run one CTA per SM anyway).
-constexpr int64_t kNrTableBytes = 16384;
+// Angles of a batch, per warp: 2 KB leave room on an SM for 16 warps with two batches and a ring each; one token of
+// the longest table (512 pairs, 4 KB) always fits, beside 7 others (rows that long run 8 warps per SM anyway).
+constexpr int64_t kNrTableBytes = 2048;
 
 template <typename T, int VEC, int NV, bool NORM, bool INTER>
 bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
   auto kernel = norm_rope_kernel<T, VEC, NV, NORM, INTER>;
-  const size_t smem = NrRing<T, VEC, NV, 1>::kBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
+  const size_t smem = NrRing<T, VEC, NV, 1>::kWarpBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return false;
-  kernel<<<(unsigned)(p.ctas * p.parts), kNrThreads, smem, st>>>(p);
+  kernel<<<(unsigned)(p.walks << p.wide_log), 32, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess;
 }
 
 template <typename T, int VEC, int NV, bool INTER>
 bool nr_launch_bwd(const NrBwdParams& p, int ctas, cudaStream_t st) {
   auto kernel = norm_rope_backward_kernel<T, VEC, NV, INTER>;
-  const size_t smem = NrRing<T, VEC, NV, 2>::kBytes +
+  const size_t smem = (size_t)kNrWarps * NrRing<T, VEC, NV, 2>::kWarpBytes +
                       std::max((size_t)2 * p.batch * p.s.pairs * sizeof(float2),
                                (size_t)kNrWarps * p.s.norm_dim * sizeof(float));
   if (smem > 48 * 1024 &&
@@ -165,8 +164,8 @@ bool nr_run(const Params& p, int dtype, int vec, int nv, int ctas, cudaStream_t 
   return dtype == LOZA_BF16 ? half(__nv_bfloat16()) : half(__half());
 }
 
-// CTAs that fill the GPU.
-int nr_ctas(int vec, int nv) { return sm_count() * nr_ctas_per_sm(vec, nv); }
+// Warps that fill the GPU.
+int64_t nr_warps(int vec, int nv) { return (int64_t)sm_count() * nr_warps_per_sm(vec, nv); }
 
 // Log2 of the warps that share a token: as many as find room beside each
 // other on the GPU's `warps`; at most `most`, and never more than the widest
@@ -177,44 +176,43 @@ int nr_wide(int64_t tokens, int64_t groups, int64_t warps, int64_t most) {
   return w;
 }
 
-// Tokens per step of a CTA, between two barriers: four per warp (or group of
-// warps) as far as the angles fit. One per warp instead of four: norm +
-// rotation of 16,381 tokens 78 against 75 us, the gradient of 32,749 201
-// against 195.
-int nr_batch(const NrShape& s, int wide_log) {
-  const int step = std::max(1, kNrWarps >> wide_log);
+// Tokens of a step of a CTA of `warps` warps, whose angles are formed together:
+// four per warp (or group of warps) as far as they fit. One per warp instead of
+// four: norm + rotation of 16,381 tokens 78 against 75 us, the gradient of
+// 32,749 201 against 195.
+int nr_batch(const NrShape& s, int warps, int wide_log) {
+  const int step = std::max(1, warps >> wide_log);
   int each = 4;
-  while (each > 1 && (int64_t)step * each * s.pairs * (int64_t)sizeof(float2) > kNrTableBytes) each /= 2;
+  while (each > 1 && (int64_t)step * each * s.pairs * (int64_t)sizeof(float2) > kNrTableBytes * warps) each /= 2;
   return step * each;
 }
 
-// The forward's walk, from the groups of the widest side and of a whole token.
-// With fewer tokens than CTAs several CTAs share a token. With many, equal
-// shares end up to 40 % apart: SMs do not get equal shares of the memory's
+// The forward's walks, from the groups of the widest side and of a whole token.
+// With fewer tokens than warps several warps share a walk. With many, equal
+// shares end up to 40 % apart: SMs do not get equal parts of the memory's
 // bandwidth (a pure copy's CTAs ended between 60 and 135 us). Short walks that
-// the hardware deals out as SMs become free even this out, but each starts with
-// an empty ring and angles to form. They pay where a warp's walk is long
-// enough: rotation of 16,411 tokens, 64 heads of 192 (32 groups) 151 -> 129 us;
-// 16,384 tokens, 32 + 8 heads of 128 into pages without weights (12 groups)
-// 77 -> 64, in fp32 with weights (24) 153 -> 128, 64 + 8 heads with weights (20)
-// 128 -> 115. Not below: with weights and 12 groups 73 -> 81, the rotation of 8
-// heads (2 groups) 65 -> 71, rows of 4-byte vectors 29 -> 33; nor with less
-// than one and a half walks per CTA (1.05: 15 -> 19).
+// the hardware deals out as warps end even this out, but each starts with an
+// empty ring and angles to form, so a token must have groups enough. Equal
+// shares / short walks, us: rotation of 16,411 tokens, 64 heads of 192 (32
+// groups, walks of 1 token) 152 / 127, 16,384 tokens, 32 heads of 128 (8; 2)
+// 53 / 46, 32 + 8 heads of 128 without weights (12; 1) 77 / 64; with weights 12
+// groups (2) 76 / 73, 20 (1) 128 / 110, in fp32 24 (1) 152 / 127. Not with fewer:
+// rotation of 8 heads (2 groups) 59 / 65, 16 + 4 heads of 256 with weights (11)
+// 71 / 73, rows of 4-byte vectors 30 / 33; nor with less than one and a half
+// walks per warp that fits (1.05: 15 / 19).
 void nr_plan_fwd(NrFwdParams* p, int vec, int nv, int size, int64_t groups, int64_t token_groups) {
-  const int64_t ctas = nr_ctas(vec, nv);
-  p->wide_log = nr_wide(p->s.tokens, groups, ctas * kNrWarps, 64);
-  p->parts = std::max(1, (1 << p->wide_log) / kNrWarps);
-  const int64_t need = ((p->s.tokens << p->wide_log) + kNrWarps - 1) / kNrWarps;  // a token or more for every warp
-  p->ctas = (int)std::max<int64_t>(1, std::min<int64_t>({p->s.tokens, ctas / p->parts, need}));
-  p->batch = nr_batch(p->s, p->wide_log);
+  const int64_t warps = nr_warps(vec, nv);
+  p->wide_log = nr_wide(p->s.tokens, groups, warps, 64);
+  p->walks = (int)std::min(p->s.tokens, warps >> p->wide_log);
+  p->batch = nr_batch(p->s, 1, p->wide_log);
   const bool norm = p->q.w || p->k.w;
-  if (vec * size == 16 && p->wide_log == 0 && token_groups >= (norm ? 16 : 8)) {
-    const int64_t least = norm ? 24 : 12;  // groups of a warp's walk
-    const int64_t walk = kNrWarps * ((least + token_groups - 1) / token_groups);
+  if (vec * size == 16 && p->wide_log == 0 && token_groups >= (norm ? 12 : 8)) {
+    const int64_t least = norm ? 20 : 12;  // groups of a walk
+    const int64_t walk = (least + token_groups - 1) / token_groups;
     const int64_t walks = (p->s.tokens + walk - 1) / walk;
-    if (walks * 2 >= ctas * 3) {
+    if (walks * 2 >= warps * 3) {
       p->walk = (int)walk;
-      p->ctas = (int)walks;
+      p->walks = (int)walks;
     }
   }
 }
@@ -519,10 +517,10 @@ loza_status loza_qk_norm_rope_backward(const loza_qk_norm_rope_backward_args* ar
   const int nv = nr_tasks(&p.s, vec);
   const int rows = 32 >> p.s.lph_log;
   const int64_t gq = (a.n_heads + rows - 1) / rows, gk = (a.n_kv_heads + rows - 1) / rows;
-  const int64_t full = nr_ctas(vec, nv);
+  const int64_t full = nr_warps(vec, nv) / kNrWarps;
   p.wide_log = nr_wide(a.tokens, std::max(gq, gk), full * kNrWarps, kNrWarps);
   const int64_t ctas = std::min(full, ((a.tokens << p.wide_log) + kNrWarps - 1) / kNrWarps);
-  p.batch = nr_batch(p.s, p.wide_log);
+  p.batch = nr_batch(p.s, kNrWarps, p.wide_log);
   if (!nr_run(p, a.dtype, vec, nv, (int)ctas, st)) return LOZA_ERR_CUDA;
   g_launches.fetch_add(1, std::memory_order_relaxed);
   if (sums) {
