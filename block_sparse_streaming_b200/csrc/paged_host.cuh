@@ -74,7 +74,7 @@ bool nr_rows_ok(const void* x, int64_t stride, int heads, int d, int size) {
 // Largest vector (in elements) that every size, offset, stride and address
 // allows: 16 bytes, for 16-bit types 4 bytes, or one element. Norm + rotation
 // of 8,192 tokens with 32 + 8 heads (bf16): heads of 128 in 16-byte vectors
-// took 41 us; heads of 100 in 4-byte vectors 75 us, element by element 150.
+// took 41 us; heads of 100 in 4-byte vectors 70 us, element by element twice that.
 int nr_vec(const NrShape& s, int size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> sizes) {
   for (int v : {16 / size, 2}) {
     if (v == 2 && size == 4) continue;
@@ -178,8 +178,8 @@ int nr_wide(int64_t tokens, int64_t groups, int64_t warps, int64_t most) {
 
 // Tokens of a step of a CTA of `warps` warps, whose angles are formed together:
 // four per warp (or group of warps) as far as they fit. One per warp instead of
-// four: norm + rotation of 16,381 tokens 78 against 75 us, the gradient of
-// 32,749 201 against 195.
+// four: the gradient of 32,749 tokens 201 against 195 us, norm + rotation of
+// 16,381 (then by CTAs of 8 warps) 78 against 75.
 int nr_batch(const NrShape& s, int warps, int wide_log) {
   const int step = std::max(1, warps >> wide_log);
   int each = 4;
