@@ -103,25 +103,35 @@ int nr_tasks(NrShape* s, int vec) {
 // the longest table (512 pairs, 4 KB) always fits, beside 7 others (rows that long run 8 warps per SM anyway).
 constexpr int64_t kNrTableBytes = 2048;
 
+// Most bytes that an instance's table of one batch takes (see nr_batch): its share per warp, or one token per warp.
+constexpr int64_t nr_most_table(int warps, int vec, int nv) {
+  return warps * std::max(kNrTableBytes, std::min<int64_t>(512, 32 * vec * nv) * (int64_t)sizeof(float2));
+}
+
 template <typename T, int VEC, int NV, bool NORM, bool INTER>
 bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
-  auto kernel = norm_rope_kernel<T, VEC, NV, NORM, INTER>;
-  const size_t smem = NrRing<T, VEC, NV, 1>::kWarpBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return false;
-  kernel<<<(unsigned)(p.walks << p.wide_log), 32, smem, st>>>(p);
+  using Ring = NrRing<T, VEC, NV, 1>;
+  static_assert(Ring::kWarpBytes + 2 * nr_most_table(1, VEC, NV) <= 48 * 1024, "no opt-in to more shared memory");
+  const size_t smem = Ring::kWarpBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
+  norm_rope_kernel<T, VEC, NV, NORM, INTER><<<(unsigned)(p.walks << p.wide_log), 32, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess;
 }
 
 template <typename T, int VEC, int NV, bool INTER>
 bool nr_launch_bwd(const NrBwdParams& p, int ctas, cudaStream_t st) {
   auto kernel = norm_rope_backward_kernel<T, VEC, NV, INTER>;
-  const size_t smem = (size_t)kNrWarps * NrRing<T, VEC, NV, 2>::kWarpBytes +
+  using Ring = NrRing<T, VEC, NV, 2>;
+  // The kernel's limit is the context's, and threads may launch other sizes of this instance at this moment: all of
+  // them set the most that the instance can ask for. (What a CTA occupies is the launch's own size.)
+  constexpr int64_t most =
+      kNrWarps * Ring::kWarpBytes +
+      std::max<int64_t>(2 * nr_most_table(kNrWarps, VEC, NV), kNrWarps * std::min(1024, 64 * VEC * NV) * sizeof(float));
+  static_assert(most <= 227 * 1024, "shared memory of a CTA");
+  const size_t smem = (size_t)kNrWarps * Ring::kWarpBytes +
                       std::max((size_t)2 * p.batch * p.s.pairs * sizeof(float2),
                                (size_t)kNrWarps * p.s.norm_dim * sizeof(float));
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  if (most > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
     return false;
   kernel<<<(unsigned)ctas, kNrThreads, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess;
@@ -302,8 +312,10 @@ loza_status loza_page_plan(const loza_page_plan_args* args, loza_stream_t stream
   p.slots = a.slots;
   p.counts = a.counts;
   const size_t smem = (size_t)(a.batch + 1) * 2 * sizeof(int);
+  // the same limit from every call: another thread's plan may be about to launch with a size of its own
+  constexpr size_t most = (size_t)(kPlanMaxBatch + 1) * 2 * sizeof(int);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem) != cudaSuccess)
+                                               (int)most) != cudaSuccess)
     return LOZA_ERR_CUDA;
   // four tokens a thread; new pages are at most one a request more than tokens / page_size
   const int64_t work = std::max<int64_t>((a.capacity + 3) / 4, a.batch);

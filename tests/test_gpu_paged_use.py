@@ -1,0 +1,106 @@
+"""How a server's or trainer's program meets the paged operators: calls from several threads at once."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged
+from test_abi_paged import NORM_ROPE_BACKWARD_ARGS, PLAN_ARGS, pack
+from test_gpu_paged import normal, plan_case, rope_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bss():
+    import block_sparse_streaming_b200 as m
+    m.build()
+    return m
+
+
+def in_threads(*bodies):
+    """The bodies at the same time; the first error of each."""
+    errors, start = [], threading.Barrier(len(bodies))
+
+    def run(body):
+        try:
+            start.wait()
+            body()
+        except Exception as e:  # handed to the test's thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(b,)) for b in bodies]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return errors
+
+
+def test_gradients_of_different_sizes_in_threads(bss):
+    """One kernel instance with more or less shared memory, launched by several threads at once through the C ABI
+    (ctypes lets go of the interpreter's lock, so the calls really meet)."""
+    L, T, d = bss.lib(), 1300, 128
+    w = normal(1, d, dtype=torch.bfloat16) + 1
+    x, dy = normal(2, T, 1, d, dtype=torch.bfloat16), normal(3, T, 1, d, dtype=torch.bfloat16)
+
+    def work(dim):
+        pos, freq, pos_d, freq_d = rope_inputs(bss, 4, T, dim)
+        want = bss.loza_qk_norm_rope_backward(dy, None, x, None, pos_d, freq_d, bss.RopeParams(dim), w)
+        st, dx, dw = torch.cuda.Stream(), torch.empty_like(x), torch.empty(d, device="cuda")
+        ws = torch.empty(L.loza_qk_norm_rope_workspace_size(d), dtype=torch.uint8, device="cuda")
+        args = pack(NORM_ROPE_BACKWARD_ARGS, dq_out=dy.data_ptr(), q=x.data_ptr(), positions=pos_d.data_ptr(),
+                    inv_freq=freq_d.data_ptr(), q_weight=w.data_ptr(), dq=dx.data_ptr(), dq_weight=dw.data_ptr(),
+                    workspace=ws.data_ptr(), workspace_bytes=ws.numel(), tokens=T, dq_out_row_stride=d, q_row_stride=d,
+                    dq_row_stride=d, n_heads=1, d=d, norm_dim=d, eps=1e-6, rope_dim=dim, rope_scale=1.0, dtype=0)
+
+        def body(keep=(pos_d, freq_d, ws)):
+            codes = set()
+            for i in range(8000):
+                codes.add(L.loza_qk_norm_rope_backward(args, st.cuda_stream))
+                if i % 100 == 99:
+                    st.synchronize()
+            assert codes == {0}, codes
+            assert torch.equal(dx, want[0]) and torch.equal(dw, want[2])
+
+        return body
+
+    bodies = [work(dim) for dim in (128, 64, 32, 2)]
+    torch.cuda.synchronize()
+    assert in_threads(*bodies) == []
+
+
+def test_plans_of_different_sizes_in_threads(bss):
+    """Plans of thousands of requests keep their sums in more or less shared memory."""
+    L = bss.lib()
+
+    def work(B):
+        ctx, new, free, table = plan_case(B, B, 16, 40, 3)
+        dev = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+        ctx_d, new_d, free_d, table_d = dev(ctx), dev(new), dev(free), dev(table)
+        capacity, st = int(new.sum()), torch.cuda.Stream()
+        want = paged.plan(ctx, new, free, table, 16, capacity)
+        cu, lens, counts = dev(np.zeros(B + 1)), dev(np.zeros(B)), dev(np.zeros(3))
+        pos, slots = dev(np.zeros(capacity)), torch.zeros(capacity, dtype=torch.int64, device="cuda")
+        args = pack(PLAN_ARGS, ctx_lens=ctx_d.data_ptr(), new_lens=new_d.data_ptr(), free_pages=free_d.data_ptr(),
+                    block_table=table_d.data_ptr(), cu_seqlens=cu.data_ptr(), seqlens=lens.data_ptr(),
+                    positions=pos.data_ptr(), slots=slots.data_ptr(), counts=counts.data_ptr(),
+                    bt_stride=table_d.stride(0), capacity=capacity, batch=B, n_free=len(free), page_size=16,
+                    max_pages=table_d.shape[1])
+
+        def body(keep=(ctx_d, new_d, free_d)):
+            codes = set()
+            for i in range(3000):
+                codes.add(L.loza_page_plan(args, st.cuda_stream))
+                if i % 100 == 99:
+                    st.synchronize()
+            assert codes == {0}, codes
+            for g, w in zip((table_d, cu, lens, pos, slots, counts), want):
+                assert (g.cpu().numpy() == w).all()
+
+        return body
+
+    bodies = [work(B) for B in (16384, 7000, 9001)]
+    torch.cuda.synchronize()
+    assert in_threads(*bodies) == []
