@@ -11,6 +11,25 @@ namespace {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Memory of a call: `rows` rows of `len` bytes, `stride` bytes apart.
+struct Extent {
+  uintptr_t at;
+  uint64_t len;
+  uint64_t rows = 1, stride = 0;
+  Extent(const void* p, uint64_t len, uint64_t rows = 1, uint64_t stride = 0)
+      : at(reinterpret_cast<uintptr_t>(p)), len(len), rows(rows), stride(stride) {}
+};
+// Whether two share a byte; b is one row.
+bool overlap(const Extent& a, const Extent& b) {
+  if (a.len == 0 || a.rows == 0 || b.len == 0) return false;
+  uint64_t r = 0;  // the first row of a that ends behind b's begin
+  if (b.at > a.at && a.rows > 1) {
+    r = (b.at - a.at) / a.stride;
+    if (b.at - a.at - r * a.stride >= a.len) ++r;
+  }
+  return r < a.rows && a.at + r * a.stride < b.at + b.len && b.at < a.at + r * a.stride + a.len;
+}
+
 // Of a power of two.
 int log2_of(int v) {
   int s = 0;
@@ -295,6 +314,21 @@ loza_status loza_page_plan(const loza_page_plan_args* args, loza_stream_t stream
   if (a.capacity > 0 && (!a.positions || !a.slots || !aligned16(a.positions) || !aligned16(a.slots)))
     return LOZA_ERR_INVALID_ARG;
   if (a.batch > kPlanMaxBatch) return LOZA_ERR_UNSUPPORTED;
+  // every CTA reads the lengths again after the first one has written seqlens: in place they would advance twice
+  const uint64_t B = a.batch, cap = a.capacity;
+  const Extent table(a.block_table, (uint64_t)a.max_pages * 4, B, (uint64_t)a.bt_stride * 4);
+  const Extent in[] = {{a.ctx_lens, B * 4}, {a.new_lens, B * 4}, {a.free_pages, (uint64_t)a.n_free * 4}};
+  const Extent out[] = {{a.cu_seqlens, (B + 1) * 4}, {a.seqlens, B * 4}, {a.counts, 12}, {a.positions, cap * 4},
+                        {a.slots, cap * 8}};
+  for (const Extent& x : in)
+    if (overlap(table, x)) return LOZA_ERR_INVALID_ARG;
+  for (const Extent& o : out) {
+    if (overlap(table, o)) return LOZA_ERR_INVALID_ARG;
+    for (const Extent& x : in)
+      if (overlap(o, x)) return LOZA_ERR_INVALID_ARG;
+    for (const Extent* x = out; x != &o; ++x)
+      if (overlap(o, *x)) return LOZA_ERR_INVALID_ARG;
+  }
   PlanParams p{};
   p.ctx = a.ctx_lens;
   p.add = a.new_lens;

@@ -504,8 +504,10 @@ typedef struct {
  * past capacity are counted but not written. A negative page number in the
  * part of the table that a request holds (a page handed back because the
  * window left it) gives slot -1. Lengths outside [0, 2^30) count as 0.
- * All pointers are device memory; positions and slots 16-byte aligned; page
- * numbers in free_pages must be distinct and not in use. max_pages <=
+ * All pointers are device memory; positions and slots 16-byte aligned. What is
+ * written (the table's rows included) must share no memory with what is read
+ * nor with each other (LOZA_ERR_INVALID_ARG): lengths do not advance in place.
+ * Page numbers in free_pages must be distinct and not in use. max_pages <=
  * bt_stride; page_size a power of two up to 65,536; at most 16,384 requests
  * (LOZA_ERR_UNSUPPORTED beyond).
  */
