@@ -313,6 +313,10 @@ loza_status loza_page_plan(const loza_page_plan_args* args, loza_stream_t stream
     return LOZA_ERR_INVALID_ARG;
   if (a.capacity > 0 && (!a.positions || !a.slots || !aligned16(a.positions) || !aligned16(a.slots)))
     return LOZA_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)a.ctx_lens, (const void*)a.new_lens, (const void*)a.free_pages,
+                        (const void*)a.block_table, (const void*)a.cu_seqlens, (const void*)a.seqlens,
+                        (const void*)a.counts})
+    if (!aligned_to(x, 4)) return LOZA_ERR_INVALID_ARG;
   if (a.batch > kPlanMaxBatch) return LOZA_ERR_UNSUPPORTED;
   // every CTA reads the lengths again after the first one has written seqlens: in place they would advance twice
   const uint64_t B = a.batch, cap = a.capacity;
@@ -588,6 +592,7 @@ loza_status loza_ssa_decode_paged_kv(const loza_decode_paged_kv_args* args, loza
   const loza_kv_pool* pool = &a.pool;
   if (!a.q || !pool->k || !pool->v || !a.block_table || !a.seqlens || !a.out || !a.lse) return LOZA_ERR_INVALID_ARG;
   if (!aligned16(a.q) || !aligned16(pool->k) || !aligned16(pool->v) || !aligned16(a.out)) return LOZA_ERR_INVALID_ARG;
+  if (!aligned_to(a.block_table, 4) || !aligned_to(a.seqlens, 4) || !aligned_to(a.lse, 4)) return LOZA_ERR_INVALID_ARG;
   if (a.batch < 1 || a.batch > 65535 || a.max_seqlen < 1 || a.max_seqlen > (1 << 30)) return LOZA_ERR_INVALID_ARG;
   if (!pool_page_ok(*pool)) return LOZA_ERR_INVALID_ARG;
   if (!pool_strides_ok(pool->k_page_stride, pool->k_row_stride, pool->k_head_stride) ||

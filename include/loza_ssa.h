@@ -504,12 +504,12 @@ typedef struct {
  * past capacity are counted but not written. A negative page number in the
  * part of the table that a request holds (a page handed back because the
  * window left it) gives slot -1. Lengths outside [0, 2^30) count as 0.
- * All pointers are device memory; positions and slots 16-byte aligned. What is
- * written (the table's rows included) must share no memory with what is read
- * nor with each other (LOZA_ERR_INVALID_ARG): lengths do not advance in place.
- * Page numbers in free_pages must be distinct and not in use. max_pages <=
- * bt_stride; page_size a power of two up to 65,536; at most 16,384 requests
- * (LOZA_ERR_UNSUPPORTED beyond).
+ * All pointers are device memory, on their type's alignment, positions and
+ * slots on 16 bytes. What is written (the table's rows included) must share no
+ * memory with what is read nor with each other (LOZA_ERR_INVALID_ARG): lengths
+ * do not advance in place. Page numbers in free_pages must be distinct and not
+ * in use. max_pages <= bt_stride; page_size a power of two up to 65,536; at
+ * most 16,384 requests (LOZA_ERR_UNSUPPORTED beyond).
  */
 typedef struct {
     const int32_t *ctx_lens, *new_lens, *free_pages;
@@ -644,8 +644,8 @@ size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, 
  * keys of all sequences together, so one long sequence and many ragged ones
  * both fill the GPU.
  *   q       [batch, n_heads, d_qk], rows q_row_stride elements apart
- *   pool    both pools given, 16-byte aligned, every stride a multiple of 8
- *           elements, page_size >= 16
+ *   pool    both pools given, 16-byte aligned (as q and out), every stride a
+ *           multiple of 8 elements, page_size >= 16
  *   block_table  device int32, page of key t of sequence n: block_table[n *
  *           bt_stride + t / page_size]; bt_stride >= ceil(max_seqlen /
  *           page_size). Only entries of pages that hold a key below

@@ -1,9 +1,9 @@
-"""What the paged operators' C entry points refuse by their pointers alone, before any launch (no GPU): outputs
-that lie on inputs which other parts of the kernel still read."""
+"""What the paged operators' C entry points refuse by their pointers alone, before any launch (no GPU): addresses
+that a kernel could not load from, and outputs that lie on inputs which other parts of the kernel still read."""
 import pytest
 
 import block_sparse_streaming_b200 as bss
-from test_abi_paged import INVALID, _plan
+from test_abi_paged import INVALID, _decode, _plan
 
 CTX, NEW, FREE, TABLE = 1 << 20, 1 << 21, 1 << 22, 1 << 23  # _plan's inputs: 4 requests, 9 free pages, 4 rows of 8
 
@@ -43,3 +43,14 @@ def test_plan_takes_neighbours(L, over):
     if torch.cuda.is_available():
         pytest.skip("would launch")
     assert _plan(L, **over) == -4
+
+
+@pytest.mark.parametrize("over", [dict(ctx=CTX + 2), dict(new=NEW + 1), dict(free=FREE + 2), dict(table=TABLE + 2),
+                                  dict(cu=(1 << 24) + 2), dict(lens=(1 << 25) + 1), dict(counts=(1 << 28) + 2)])
+def test_plan_refuses_misaligned_pointers(L, over):
+    assert refused(L, _plan, **over)
+
+
+@pytest.mark.parametrize("over", [dict(bt=(1 << 21) + 2), dict(lens=(1 << 22) + 1), dict(lse=(1 << 24) + 2)])
+def test_decode_refuses_misaligned_pointers(L, over):
+    assert refused(L, _decode, **over)
