@@ -33,6 +33,7 @@ decltype(&loza_qk_norm_rope_workspace_size) f_norm_rope_workspace;
 decltype(&loza_ssa_decode_paged_kv) f_decode;
 decltype(&loza_decode_paged_kv_workspace_size) f_decode_workspace;
 PyObject* g_status_error;  // LozaError(status, what)
+PyObject *g_rope_params, *g_window_params;  // the classes RopeParams and Params
 
 // What a call cannot take: raised as TypeError or ValueError; a status of the C ABI as LozaError.
 struct Refused {
@@ -70,20 +71,23 @@ double number(PyObject* o) {
   return v;
 }
 
-// RopeParams and Params are ctypes structures laid out like the C ones.
+// RopeParams and Params are ctypes structures laid out like the C ones, of the same size: their class tells them apart.
 template <typename T>
-T params(PyObject* o, const char* name) {
+T params(PyObject* o, PyObject* type, const char* what) {
+  const int is = PyObject_IsInstance(o, type);
+  if (is < 0) throw PythonError{};
+  if (!is) type_error(what);
   Py_buffer b;
-  if (!PyObject_CheckBuffer(o) || PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) {
-    PyErr_Clear();
-    type_error(std::string(name) + " must be this package's parameter structure");
-  }
+  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) throw PythonError{};
   T v;
   const bool fits = b.len == (Py_ssize_t)sizeof(T);
   if (fits) memcpy(&v, b.buf, sizeof(T));
   PyBuffer_Release(&b);
-  if (!fits) type_error(std::string(name) + " must be this package's parameter structure");
+  if (!fits) type_error(what);
   return v;
+}
+loza_rope_params rope_params(PyObject* o) {
+  return params<loza_rope_params>(o, g_rope_params, "rope must be a RopeParams");
 }
 
 // A call's device, from its first tensor; made current for the call.
@@ -317,8 +321,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 template <typename P>
-void rope_tables(P* p, PyObject* positions, PyObject* inv_freq, PyObject* rope, const Place& at, int64_t tokens) {
-  p->rope = params<loza_rope_params>(rope, "rope");
+void rope_tables(P* p, PyObject* positions, PyObject* inv_freq, const Place& at, int64_t tokens) {
   p->positions = static_cast<int32_t*>(plain(positions, "positions", at, at::kInt, {tokens}));
   p->inv_freq = static_cast<double*>(plain(inv_freq, "inv_freq", at, at::kDouble, {std::max(0, p->rope.rope_dim / 2)}));
 }
@@ -327,12 +330,13 @@ void rope_tables(P* p, PyObject* positions, PyObject* inv_freq, PyObject* rope, 
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
     expect(n, 6);
+    loza_rope_args p{};
+    p.rope = rope_params(a[3]);
     const at::Tensor& x = rank(a[0], "x", 3);
     const Place at(x, "x");
-    loza_rope_args p{};
     p.dtype = dtype_code(x, "x");
     const int64_t T = x.size(0);
-    rope_tables(&p, a[1], a[2], a[3], at, T);
+    rope_tables(&p, a[1], a[2], at, T);
     const Rows xr(x, "x", at, x.scalar_type(), x.sizes());
     Output out;
     const Rows orow = rows_out(&out, a[4], "out", at, x.scalar_type(), x.sizes());
@@ -370,11 +374,12 @@ int64_t given_norm_dim(PyObject* o) {
 PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
     expect(n, 15);
+    loza_qk_norm_rope_args p{};
+    p.rope = rope_params(a[4]);
     const bool has_q = !none(a[0]), has_k = !none(a[1]), has_v = !none(a[8]), has_pool = !none(a[9]);
     const at::Tensor& first = has_q ? rank(a[0], "q", 3) : rank(a[1], "k", 3);
     const Place at(first, has_q ? "q" : "k");
     const at::ScalarType dtype = first.scalar_type();
-    loza_qk_norm_rope_args p{};
     p.dtype = dtype_code(first, has_q ? "q" : "k");
     const int64_t T = first.size(0), d = first.size(2);
     p.tokens = T;
@@ -422,7 +427,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (has_v || !none(a[10]) || !none(a[11])) {
       value_error("v, v_pool and slots need k_pool");
     }
-    rope_tables(&p, a[2], a[3], a[4], at, T);
+    rope_tables(&p, a[2], a[3], at, T);
     int64_t norm_dim = given_norm_dim(a[14]);
     p.q_weight = weight(a[5], has_q, "q_weight", &norm_dim, at, dtype);
     p.k_weight = weight(a[6], has_k, "k_weight", &norm_dim, at, dtype);
@@ -437,11 +442,12 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
     expect(n, 14);
+    loza_qk_norm_rope_backward_args p{};
+    p.rope = rope_params(a[6]);
     const bool has_q = !none(a[0]), has_k = !none(a[1]);
     const at::Tensor& first = has_q ? rank(a[0], "dq_out", 3) : rank(a[1], "dk_out", 3);
     const Place at(first, has_q ? "dq_out" : "dk_out");
     const at::ScalarType dtype = first.scalar_type();
-    loza_qk_norm_rope_backward_args p{};
     p.dtype = dtype_code(first, has_q ? "dq_out" : "dk_out");
     const int64_t T = first.size(0), d = first.size(2);
     p.tokens = T;
@@ -490,7 +496,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (!none(a[11])) {
       value_error("dk without dk_out");
     }
-    rope_tables(&p, a[4], a[5], a[6], at, T);
+    rope_tables(&p, a[4], a[5], at, T);
     p.eps = (float)number(a[9]);
     if (p.q_weight || p.k_weight)
       p.workspace = workspace(a[13], at, f_norm_rope_workspace(p.norm_dim), &ws, &p.workspace_bytes);
@@ -504,10 +510,11 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* decode_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
     expect(n, 10);
+    loza_decode_paged_kv_args p{};
+    p.window = params<loza_ssa_params>(a[6], g_window_params, "params must be a Params");
     const at::Tensor& q = rank(a[0], "q", 3);
     const Place at(q, "q");
     const at::ScalarType dtype = q.scalar_type();
-    loza_decode_paged_kv_args p{};
     p.dtype = dtype_code(q, "q");
     const int64_t B = q.size(0), H = q.size(1), d = q.size(2);
     const Rows r(q, "q", at, dtype, q.sizes());
@@ -526,7 +533,6 @@ PyObject* decode_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.seqlens = static_cast<int32_t*>(plain(a[4], "seqlens", at, at::kInt, {B}));
     p.max_seqlen = int32(a[5], "max_seqlen");
     if (table.cols * p.pool.page_size < p.max_seqlen) value_error("block_table has too few columns for max_seqlen");
-    p.window = params<loza_ssa_params>(a[6], "params");
     Output out, lse;
     at::Tensor ws;
     if (none(a[7])) {
@@ -550,10 +556,10 @@ PyObject* decode_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// ({name: address}, LozaError)
+// ({name: address}, LozaError, RopeParams, Params)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
-    expect(n, 2);
+    expect(n, 4);
     auto at = [&](const char* name) {
       PyObject* v = PyDict_Check(a[0]) ? PyDict_GetItemString(a[0], name) : nullptr;
       if (!v) type_error(std::string("no address of ") + name);
@@ -567,6 +573,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     f_decode = reinterpret_cast<decltype(f_decode)>(at("loza_ssa_decode_paged_kv"));
     f_decode_workspace = reinterpret_cast<decltype(f_decode_workspace)>(at("loza_decode_paged_kv_workspace_size"));
     g_status_error = Py_NewRef(a[1]);
+    g_rope_params = Py_NewRef(a[2]);
+    g_window_params = Py_NewRef(a[3]);
     return Py_NewRef(Py_None);
   });
 }

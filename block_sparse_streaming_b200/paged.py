@@ -22,9 +22,6 @@ from . import _paged_binding as _c  # noqa: E402
 if _c.torch_version != torch.__version__:
     raise RuntimeError(f"{BINDING_PATH} was built for torch {_c.torch_version}, not {torch.__version__}: remove it and "
                        "run block_sparse_streaming_b200.build()")
-_c.bind({name: ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
-    "loza_page_plan", "loza_rope", "loza_qk_norm_rope", "loza_qk_norm_rope_backward",
-    "loza_qk_norm_rope_workspace_size", "loza_ssa_decode_paged_kv", "loza_decode_paged_kv_workspace_size")}, LozaError)
 
 LOZA_BF16, LOZA_FP16, LOZA_FP32 = 0, 1, 2
 _SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}  # LOZA_ROPE_*
@@ -39,6 +36,12 @@ class RopeParams(ctypes.Structure):
 
     def __init__(self, rope_dim: int, rope_offset: int = 0, interleaved: bool = False, scale: float = 1.0):
         super().__init__(rope_dim, rope_offset, int(bool(interleaved)), scale)
+
+
+_c.bind({name: ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
+    "loza_page_plan", "loza_rope", "loza_qk_norm_rope", "loza_qk_norm_rope_backward",
+    "loza_qk_norm_rope_workspace_size", "loza_ssa_decode_paged_kv", "loza_decode_paged_kv_workspace_size")},
+    LozaError, RopeParams, Params)
 
 
 def _on(stream, call, *args):

@@ -1,4 +1,4 @@
-"""How a server's or trainer's program meets the paged operators: calls from several threads at once."""
+"""How a server's or trainer's program meets the paged operators: calls from several threads at once, and with arguments mixed up."""
 import threading
 
 import numpy as np
@@ -104,3 +104,26 @@ def test_plans_of_different_sizes_in_threads(bss):
     bodies = [work(B) for B in (16384, 7000, 9001)]
     torch.cuda.synchronize()
     assert in_threads(*bodies) == []
+
+
+def test_exchanged_structures_are_refused(bss):
+    """Params and RopeParams have the same size: each is taken only where it belongs, and nothing else is."""
+    q = normal(1, 2, 8, 64, dtype=torch.bfloat16)
+    pool = normal(2, 4, 16, 8, 64, dtype=torch.bfloat16)
+    pos, freq, pos_d, freq_d = rope_inputs(bss, 1, 2, 64)
+    table = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    window, rope = bss.Params(1.0, 64, 0, 1), bss.RopeParams(64, 0, True)
+    decode = lambda p: bss.loza_ssa_decode_paged_kv(q, pool, pool, table, pos_d.clamp(0, 9), 9, p)
+    rotate = lambda r: bss.loza_rope(q, pos_d, freq_d, r)
+    norm = lambda r: bss.loza_qk_norm_rope(q, None, pos_d, freq_d, r)
+    grad = lambda r: bss.loza_qk_norm_rope_backward(q, None, None, None, pos_d, freq_d, r)
+    decode(window), rotate(rope), norm(rope), grad(rope)
+    before = bss.launch_count()
+    for bad in (rope, bytes(rope), bytearray(bytes(window)), torch.zeros(4).numpy(), None):
+        with pytest.raises(TypeError):
+            decode(bad)
+    for call in (rotate, norm, grad):
+        for bad in (window, bytes(rope), torch.zeros(4).numpy(), None):
+            with pytest.raises(TypeError):
+                call(bad)
+    assert bss.launch_count() == before
