@@ -33,6 +33,7 @@ decltype(&loza_qk_norm_rope_workspace_size) f_norm_rope_workspace;
 decltype(&loza_ssa_decode_paged_kv) f_decode;
 decltype(&loza_decode_paged_kv_workspace_size) f_decode_workspace;
 PyObject* g_status_error;  // LozaError(status, what)
+PyObject* g_memory_error;  // torch.OutOfMemoryError
 PyObject *g_rope_params, *g_window_params;  // the classes RopeParams and Params
 
 // What a call cannot take: raised as TypeError or ValueError; a status of the C ABI as LozaError.
@@ -263,7 +264,11 @@ PyObject* guarded(F&& body) {
       Py_DECREF(v);
     }
   } catch (const PythonError&) {
-  } catch (const std::exception& e) {  // torch: out of memory and the like
+  } catch (const c10::OutOfMemoryError& e) {  // as from torch.empty: callers free memory and go on
+    PyErr_SetString(g_memory_error, e.what_without_backtrace());
+  } catch (const c10::Error& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+  } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
@@ -556,10 +561,10 @@ PyObject* decode_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// ({name: address}, LozaError, RopeParams, Params)
+// ({name: address}, LozaError, RopeParams, Params, torch.OutOfMemoryError)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&] {
-    expect(n, 4);
+    expect(n, 5);
     auto at = [&](const char* name) {
       PyObject* v = PyDict_Check(a[0]) ? PyDict_GetItemString(a[0], name) : nullptr;
       if (!v) type_error(std::string("no address of ") + name);
@@ -575,6 +580,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_status_error = Py_NewRef(a[1]);
     g_rope_params = Py_NewRef(a[2]);
     g_window_params = Py_NewRef(a[3]);
+    g_memory_error = Py_NewRef(a[4]);
     return Py_NewRef(Py_None);
   });
 }

@@ -41,7 +41,7 @@ class RopeParams(ctypes.Structure):
 _c.bind({name: ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
     "loza_page_plan", "loza_rope", "loza_qk_norm_rope", "loza_qk_norm_rope_backward",
     "loza_qk_norm_rope_workspace_size", "loza_ssa_decode_paged_kv", "loza_decode_paged_kv_workspace_size")},
-    LozaError, RopeParams, Params)
+    LozaError, RopeParams, Params, torch.OutOfMemoryError)
 
 
 def _on(stream, call, *args):

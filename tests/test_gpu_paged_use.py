@@ -1,4 +1,5 @@
-"""How a server's or trainer's program meets the paged operators: calls from several threads at once, and with arguments mixed up."""
+"""How a server's or trainer's program meets the paged operators: calls from several threads at once,
+with arguments mixed up, and short of memory."""
 import threading
 
 import numpy as np
@@ -127,3 +128,24 @@ def test_exchanged_structures_are_refused(bss):
             with pytest.raises(TypeError):
                 call(bad)
     assert bss.launch_count() == before
+
+
+def test_out_of_memory_is_torchs_error(bss):
+    """An output or workspace that does not fit raises what torch.empty raises (the allocator's own limit, set low)."""
+    x = normal(1, 4000, 8, 128, dtype=torch.bfloat16)
+    pos, freq, pos_d, freq_d = rope_inputs(bss, 1, 4000, 128)
+    i32 = torch.zeros(1, dtype=torch.int32, device="cuda")
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 22)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+        with pytest.raises(torch.OutOfMemoryError):
+            bss.loza_page_plan(i32, i32, i32, i32.view(1, 1), 16, 1 << 24)
+        with pytest.raises(torch.OutOfMemoryError):
+            y = [bss.loza_rope(x, pos_d, freq_d, bss.RopeParams(128)) for _ in range(4)]
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    y = bss.loza_rope(x, pos_d, freq_d, bss.RopeParams(128))
+    assert y.shape == x.shape
