@@ -152,12 +152,21 @@ const at::Tensor& rank(PyObject* o, const char* name, int64_t dims) {
   return t;
 }
 
+// A tensor that a call has written in place: autograd then notices that what it had saved of it is gone. (Tensors of
+// inference mode keep no count.)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // An output: the caller's (checked) or a new one; `made` keeps a new one until it is wrapped.
 struct Output {
   PyObject* given = nullptr;
   at::Tensor made;
   PyObject* take() {
-    if (given) return Py_NewRef(given);
+    if (given) {
+      written(THPVariable_Unpack(given));
+      return Py_NewRef(given);
+    }
     return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(Py_None);
   }
 };
@@ -319,6 +328,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.positions = pos.data_ptr<int32_t>();
     p.slots = slots.data_ptr<int64_t>();
     call(f_page_plan, p, at, "loza_page_plan");
+    written(THPVariable_Unpack(a[3]));
     return tuple({THPVariable_Wrap(std::move(cu)), THPVariable_Wrap(std::move(lens)),
                   THPVariable_Wrap(std::move(pos)), THPVariable_Wrap(std::move(slots)),
                   THPVariable_Wrap(std::move(counts))});
@@ -439,6 +449,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.norm_dim = dim32(std::max<int64_t>(0, norm_dim));
     p.eps = (float)number(a[7]);
     call(f_norm_rope, p, at, "loza_qk_norm_rope");
+    if (has_pool) written(THPVariable_Unpack(a[9]));
+    if (has_pool && has_v) written(THPVariable_Unpack(a[10]));
     return tuple({q_out.take(), k_out.take()});
   });
 }

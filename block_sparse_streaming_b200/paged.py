@@ -4,7 +4,11 @@ heads with their gradient, decode over paged K and V pools.
 The package re-exports these names. Marshalling only, like the rest of the binding; checks, outputs and the call of
 the C ABI are in the compiled part (csrc/paged_binding.cpp), because the calls are a few microseconds long. Every
 tensor of a call lives on one GPU, which need not be the current one; with `stream` the whole call runs there, its
-buffers included. Nothing is read back to the host, and every call can be captured into a graph."""
+buffers included. Nothing is read back to the host, and every call can be captured into a graph.
+
+The calls record no autograd graph, whether their inputs require gradients or not: a training step calls the gradient
+(loza_qk_norm_rope_backward; loza_rope with transposed) itself. What a call writes in place (out, pools, the block
+table) counts as modified, so autograd refuses a backward that had saved it."""
 from __future__ import annotations
 
 import ctypes

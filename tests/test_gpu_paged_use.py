@@ -1,5 +1,5 @@
 """How a server's or trainer's program meets the paged operators: calls from several threads at once,
-with arguments mixed up, and short of memory."""
+with arguments mixed up, short of memory, and beside autograd."""
 import threading
 
 import numpy as np
@@ -149,3 +149,45 @@ def test_out_of_memory_is_torchs_error(bss):
         torch.cuda.set_per_process_memory_fraction(1.0)
     y = bss.loza_rope(x, pos_d, freq_d, bss.RopeParams(128))
     assert y.shape == x.shape
+
+
+def test_written_tensors_count_their_versions(bss):
+    """What a call writes in place counts as changed, so that autograd notices a saved tensor that was overwritten;
+    what it reads does not, and tensors of inference mode, which keep no count, are taken."""
+    T, H, Hk, d, P = 6, 4, 2, 64, 16
+    dt = torch.bfloat16
+    pos, freq, pos_d, freq_d = rope_inputs(bss, 1, T, d)
+    rope, w = bss.RopeParams(d), normal(9, d, dtype=dt) + 1
+    q, k, v, gq, gk = (normal(s, T, h, d, dtype=dt) for s, h in enumerate((H, Hk, Hk, H, Hk)))
+    kp, vp = (normal(7, 4, P, Hk, d, dtype=dt) for _ in range(2))
+    slots, lens = torch.arange(T, device="cuda"), torch.full((T,), 3, dtype=torch.int32, device="cuda")
+    table = torch.zeros(T, 2, dtype=torch.int32, device="cuda")
+    free = torch.arange(3, 40, dtype=torch.int32, device="cuda")
+    out, lse = torch.empty(T, H, d, dtype=dt, device="cuda"), torch.empty(T, H, device="cuda")
+    dq, dk = torch.empty_like(q), torch.empty_like(k)
+    q2 = q.clone()
+    p = bss.Params(0.1, 128, 0, -1)
+    calls = [
+        (lambda: bss.loza_rope(q, pos_d, freq_d, rope, out=q), [q], [pos_d, freq_d]),
+        (lambda: bss.loza_rope(q, pos_d, freq_d, rope), [], [q]),
+        (lambda: bss.loza_qk_norm_rope(q, k, pos_d, freq_d, rope, w, w, v=v, k_pool=kp, v_pool=vp, slots=slots, q_out=q,
+                                       k_out=k), [q, k, kp, vp], [v, w, slots]),
+        (lambda: bss.loza_qk_norm_rope_backward(gq, gk, q, k, pos_d, freq_d, rope, w, w, dq=dq, dk=dk), [dq, dk],
+         [gq, gk, q, k, w]),
+        (lambda: bss.loza_ssa_decode_paged_kv(q2, kp, vp, table, lens, 3, p, out=out, lse=lse), [out, lse],
+         [q2, kp, vp, table, lens]),
+        (lambda: bss.loza_page_plan(lens, lens, free, table, P, 40), [table], [lens, free])]
+    for call, written, read in calls:
+        before = [t._version for t in written], [t._version for t in read]
+        call()
+        assert all(t._version > n for t, n in zip(written, before[0]))
+        assert [t._version for t in read] == before[1]
+    x = normal(11, T, H, d).requires_grad_()
+    y = x * 2
+    z = (y * y).sum()  # keeps y
+    bss.loza_rope(y.detach(), pos_d, freq_d, rope, out=y.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
+    with torch.inference_mode():
+        a = q.clone()
+        assert bss.loza_rope(a, pos_d, freq_d, rope, out=a) is a
