@@ -225,8 +225,9 @@ void pool_side(loza_kv_pool* pool, bool values, PyObject* o, const Place& at, at
     value_error("k_pool and v_pool must have the same pages");
   }
   (values ? pool->v : pool->k) = t.data_ptr();
-  (values ? pool->v_page_stride : pool->k_page_stride) = s[0];
-  (values ? pool->v_row_stride : pool->k_row_stride) = s[1];
+  // the stride of a dimension of one is never used and may be anything
+  (values ? pool->v_page_stride : pool->k_page_stride) = t.size(0) > 1 ? s[0] : 0;
+  (values ? pool->v_row_stride : pool->k_row_stride) = t.size(1) > 1 ? s[1] : 0;
   (values ? pool->v_head_stride : pool->k_head_stride) = heads > 1 ? s[2] : 0;
 }
 

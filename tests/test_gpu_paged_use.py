@@ -1,5 +1,5 @@
 """How a server's or trainer's program meets the paged operators: calls from several threads at once,
-with arguments mixed up, short of memory, and beside autograd."""
+with arguments mixed up, short of memory, beside autograd, and with a pool of one page."""
 import threading
 
 import numpy as np
@@ -191,3 +191,22 @@ def test_written_tensors_count_their_versions(bss):
     with torch.inference_mode():
         a = q.clone()
         assert bss.loza_rope(a, pos_d, freq_d, rope, out=a) is a
+
+
+def test_pool_of_one_page_has_any_page_stride(bss):
+    """The stride of a dimension of size one is never used, whatever the tensor says it is."""
+    T, Hk, d, P = 5, 2, 64, 16
+    dt = torch.bfloat16
+    pos, freq, pos_d, freq_d = rope_inputs(bss, 1, T, d)
+    k = normal(1, T, Hk, d, dtype=dt)
+    slots = torch.arange(T, device="cuda")
+    pools = [torch.zeros(1, P, Hk, d, dtype=dt, device="cuda") for _ in range(2)]
+    odd = [t.as_strided(t.shape, (3, *t.stride()[1:])) for t in pools]
+    bss.loza_qk_norm_rope(None, k, pos_d, freq_d, bss.RopeParams(d), v=k, k_pool=odd[0], v_pool=odd[1], slots=slots)
+    q = normal(2, 1, 4, d, dtype=dt)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.full((1,), T, dtype=torch.int32).cuda()
+    p = bss.Params(0.1, 128, 0, -1)
+    want = bss.loza_ssa_decode_paged_kv(q, *pools, table, lens, T, p)
+    got = bss.loza_ssa_decode_paged_kv(q, *odd, table, lens, T, p)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(pools[1][0, :T], k)
