@@ -11,6 +11,7 @@ import glob
 import os
 import shutil
 import subprocess
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -79,11 +80,19 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/loza_ssa.cu (which includes every kernel) into libloza_ssa.so, and the binding."""
+    """Compile csrc/loza_ssa.cu (which includes every kernel) into libloza_ssa.so, and the binding.
+
+    The library needs nvcc alone. Where the binding cannot be compiled (no g++, Python or torch headers) the entry
+    points that do not use it work all the same: a warning says what is missing, and the others raise."""
     if force or not up_to_date():
         _compile([_nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-o", "{out}",
                   os.path.join(CSRC, "loza_ssa.cu")], LIB_PATH, verbose)
-    build_binding(force, verbose)
+    try:
+        build_binding(force, verbose)
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(BINDING_PATH):  # of another source: its argument structs may not be the library's
+            os.remove(BINDING_PATH)
+        warnings.warn(f"{os.path.basename(BINDING_PATH)} could not be built, the paged operators are not there: {e}")
     return LIB_PATH
 
 

@@ -20,7 +20,8 @@ from . import LozaError, Params, lib
 from ._build import BINDING_PATH
 
 if not os.path.exists(BINDING_PATH):
-    raise RuntimeError(f"{BINDING_PATH} is missing: run block_sparse_streaming_b200.build(); there is no fallback path")
+    raise RuntimeError(f"{BINDING_PATH} is missing: run block_sparse_streaming_b200.build() (a warning says why it "
+                       "cannot be built); there is no fallback path")
 from . import _paged_binding as _c  # noqa: E402
 
 if _c.torch_version != torch.__version__:
