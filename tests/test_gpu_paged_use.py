@@ -138,9 +138,12 @@ def test_out_of_memory_is_torchs_error(bss):
     total = torch.cuda.get_device_properties(0).total_memory
     torch.cuda.empty_cache()
     torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 22)) / total)
+    held = []
     try:
-        with pytest.raises(torch.OutOfMemoryError):
-            torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+        for size in (1 << 25, 1 << 22, 1 << 21):  # what the allocator kept of earlier tests
+            with pytest.raises(torch.OutOfMemoryError):
+                while True:
+                    held.append(torch.empty(size, dtype=torch.uint8, device="cuda"))
         with pytest.raises(torch.OutOfMemoryError):
             bss.loza_page_plan(i32, i32, i32, i32.view(1, 1), 16, 1 << 24)
         with pytest.raises(torch.OutOfMemoryError):
