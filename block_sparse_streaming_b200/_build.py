@@ -11,7 +11,9 @@ import glob
 import os
 import shutil
 import subprocess
+import tempfile
 import warnings
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,7 +26,7 @@ BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC",
+    "-Xcompiler", "-fPIC",
     "-Xptxas", "-v",
 ]
 
@@ -79,16 +81,26 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     return BINDING_PATH
 
 
+def _build_library(verbose: bool):
+    nvcc, units = _nvcc(), sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(os.cpu_count()) as pool:
+        objects = [os.path.join(tmp, os.path.basename(u) + ".o") for u in units]
+        list(pool.map(lambda u, o: _compile([nvcc, *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", "-o", "{out}", u],
+                                            o, verbose), units, objects))
+        _compile([nvcc, *NVCC_FLAGS[:2], "-shared", "-o", "{out}", *objects], LIB_PATH, verbose)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/loza_ssa.cu (which includes every kernel) into libloza_ssa.so, and the binding.
+    """Compile csrc/*.cu into libloza_ssa.so and the binding, each file by a compiler of its own at the same time.
 
     The library needs nvcc alone. Where the binding cannot be compiled (no g++, Python or torch headers) the entry
     points that do not use it work all the same: a warning says what is missing, and the others raise."""
-    if force or not up_to_date():
-        _compile([_nvcc(), *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-o", "{out}",
-                  os.path.join(CSRC, "loza_ssa.cu")], LIB_PATH, verbose)
+    with ThreadPoolExecutor(1) as beside:
+        binding = beside.submit(build_binding, force, verbose)
+        if force or not up_to_date():
+            _build_library(verbose)
     try:
-        build_binding(force, verbose)
+        binding.result()
     except (ImportError, OSError, RuntimeError) as e:
         if os.path.exists(BINDING_PATH):  # of another source: its argument structs may not be the library's
             os.remove(BINDING_PATH)

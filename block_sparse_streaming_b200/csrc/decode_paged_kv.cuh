@@ -34,7 +34,7 @@
 
 #include <cuda_fp16.h>
 
-#include "norm_rope.cuh"
+#include "cp_async.cuh"
 #include "prefill.cuh"
 #include "sm100.cuh"
 
@@ -575,5 +575,9 @@ __global__ void __launch_bounds__(256) decode_paged_join_kernel(const PagedKvPar
   reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * DV)[tid] = Mma16<T>::pack(x * inv, y * inv);
   if (tid == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
+
+// Both kernels for a call (decode_paged_kv.cu); false if a launch failed.
+template <typename T>
+bool pkv_run(const PagedKvParams& p, int d_qk, cudaStream_t st);
 
 }  // namespace loza

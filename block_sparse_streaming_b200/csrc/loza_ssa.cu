@@ -24,8 +24,10 @@
 #include "backward.cuh"
 #include "hi_index.cuh"
 #include "page_plan.cuh"
-#include "norm_rope.cuh"
+#include "norm_rope_launch.cuh"
+#include "norm_rope_sums.cuh"
 #include "decode_paged_kv.cuh"
+#include "launch_after.cuh"
 
 namespace loza {
 namespace {

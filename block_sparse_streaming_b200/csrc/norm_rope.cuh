@@ -17,8 +17,8 @@
 //     dn = R^T dy,  g = w dn,  dx = (g - u mean(g u)) / rms,  dw = sum dn u
 // (columns without norm: dx = dn). Weight gradients are summed in registers
 // over a warp's rows, then over the CTA's warps, then over the CTAs by
-// norm_rope_dw_kernel, each in a fixed order: no atomics, the same bits every
-// run for one GPU.
+// norm_rope_dw_kernel (norm_rope_sums.cuh), each in a fixed order: no atomics,
+// the same bits every run for one GPU.
 //
 // Both are bound by HBM: every row is read once and written once. A task is a
 // pair of 16-byte vectors of one row (for rotated columns the two halves of
@@ -41,6 +41,7 @@
 
 #include <cuda_fp16.h>
 
+#include "cp_async.cuh"
 #include "sm100.cuh"
 
 namespace loza {
@@ -384,18 +385,6 @@ __device__ __forceinline__ float nr_row_sum(float v, int lph) {
   for (int o = lph >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-// BYTES (16 or 4) global -> shared; n = 0 fills with zeros and reads nothing, else n = BYTES.
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, uint32_t n) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // A lane's ring of groups: `STREAMS` tensors, NV tasks of two vectors each.
 // Slot layout [slot][vector][lane]: neighbouring lanes are neighbouring
@@ -904,38 +893,6 @@ __global__ void __launch_bounds__(kNrThreads, nr_ctas_per_sm(VEC, NV)) norm_rope
     }
   }
   griddep_launch_dependents();
-}
-
-// dw[side][c] = sum over the CTAs of partial[side][cta][c], in a fixed order:
-// 8 columns per block, 64 threads per column each over every 64th CTA, so that
-// the few loads of a thread are all in flight at once.
-struct NrDwParams {
-  const float* partial;
-  float *dqw, *dkw;
-  int norm_dim, ctas;
-};
-__global__ void __launch_bounds__(512) norm_rope_dw_kernel(const NrDwParams p) {
-  __shared__ float part[64][9];
-  const int x = threadIdx.x & 7, col = blockIdx.x * 8 + x, j = threadIdx.x >> 3;
-  float* out = blockIdx.y == 0 ? p.dqw : p.dkw;
-  griddep_wait();
-  if (!out) return;
-  const float* in = p.partial + (size_t)blockIdx.y * p.ctas * p.norm_dim;
-  float t = 0.f;
-  if (col < p.norm_dim) {
-#pragma unroll 8
-    for (int c = j; c < p.ctas; c += 64) t += in[(size_t)c * p.norm_dim + col];
-  }
-  part[j][x] = t;
-  __syncthreads();
-  if (j < 4) {  // 16 parts each, then the four
-    t = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) t += part[j * 16 + k][x];
-    t += __shfl_xor_sync(0xffffffffu, t, 8);
-    t += __shfl_xor_sync(0xffffffffu, t, 16);
-    if (j == 0 && col < p.norm_dim) out[col] = t;
-  }
 }
 
 }  // namespace loza

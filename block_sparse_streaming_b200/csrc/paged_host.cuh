@@ -7,6 +7,10 @@
 #include <cmath>
 
 namespace loza {
+LOZA_NR_INSTANCES(extern, float);
+LOZA_NR_INSTANCES(extern, __half);
+LOZA_NR_INSTANCES(extern, __nv_bfloat16);
+
 namespace {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -35,21 +39,6 @@ int log2_of(int v) {
   int s = 0;
   while ((1 << s) < v) ++s;
   return s;
-}
-
-// A kernel behind the one that writes what it reads (it waits for it itself).
-template <typename P>
-bool launch_after(void (*kernel)(P), dim3 grid, unsigned threads, cudaStream_t st, const P& prm) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, prm) == cudaSuccess;
 }
 
 // ---------------------------------------------------------------------------
@@ -118,79 +107,11 @@ int nr_tasks(NrShape* s, int vec) {
   return nv;
 }
 
-// Angles of a batch, per warp: 2 KB leave room on an SM for 16 warps with two batches and a ring each; one token of
-// the longest table (512 pairs, 4 KB) always fits, beside 7 others (rows that long run 8 warps per SM anyway).
-constexpr int64_t kNrTableBytes = 2048;
-
-// Most bytes that an instance's table of one batch takes (see nr_batch): its share per warp, or one token per warp.
-constexpr int64_t nr_most_table(int warps, int vec, int nv) {
-  return warps * std::max(kNrTableBytes, std::min<int64_t>(512, 32 * vec * nv) * (int64_t)sizeof(float2));
-}
-
-template <typename T, int VEC, int NV, bool NORM, bool INTER>
-bool nr_launch_fwd(const NrFwdParams& p, cudaStream_t st) {
-  using Ring = NrRing<T, VEC, NV, 1>;
-  static_assert(Ring::kWarpBytes + 2 * nr_most_table(1, VEC, NV) <= 48 * 1024, "no opt-in to more shared memory");
-  const size_t smem = Ring::kWarpBytes + (size_t)2 * p.batch * p.s.pairs * sizeof(float2);
-  norm_rope_kernel<T, VEC, NV, NORM, INTER><<<(unsigned)(p.walks << p.wide_log), 32, smem, st>>>(p);
-  return cudaGetLastError() == cudaSuccess;
-}
-
-template <typename T, int VEC, int NV, bool INTER>
-bool nr_launch_bwd(const NrBwdParams& p, int ctas, cudaStream_t st) {
-  auto kernel = norm_rope_backward_kernel<T, VEC, NV, INTER>;
-  using Ring = NrRing<T, VEC, NV, 2>;
-  // The kernel's limit is the context's, and threads may launch other sizes of this instance at this moment: all of
-  // them set the most that the instance can ask for. (What a CTA occupies is the launch's own size.)
-  constexpr int64_t most =
-      kNrWarps * Ring::kWarpBytes +
-      std::max<int64_t>(2 * nr_most_table(kNrWarps, VEC, NV), kNrWarps * std::min(1024, 64 * VEC * NV) * sizeof(float));
-  static_assert(most <= 227 * 1024, "shared memory of a CTA");
-  const size_t smem = (size_t)kNrWarps * Ring::kWarpBytes +
-                      std::max((size_t)2 * p.batch * p.s.pairs * sizeof(float2),
-                               (size_t)kNrWarps * p.s.norm_dim * sizeof(float));
-  if (most > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
-    return false;
-  kernel<<<(unsigned)ctas, kNrThreads, smem, st>>>(p);
-  return cudaGetLastError() == cudaSuccess;
-}
-
-// One element per vector: both layouts are one kernel, and the rotation alone is the kernel of the norm.
-template <typename T, int VEC, int NV>
-bool nr_launch(const NrFwdParams& p, int, cudaStream_t st) {
-  const bool norm = p.q.w || p.k.w;
-  if constexpr (VEC == 1) return nr_launch_fwd<T, VEC, NV, true, false>(p, st);
-  else if (p.s.interleaved)
-    return norm ? nr_launch_fwd<T, VEC, NV, true, true>(p, st) : nr_launch_fwd<T, VEC, NV, false, true>(p, st);
-  else
-    return norm ? nr_launch_fwd<T, VEC, NV, true, false>(p, st) : nr_launch_fwd<T, VEC, NV, false, false>(p, st);
-}
-template <typename T, int VEC, int NV>
-bool nr_launch(const NrBwdParams& p, int ctas, cudaStream_t st) {
-  if constexpr (VEC == 1) return nr_launch_bwd<T, VEC, NV, false>(p, ctas, st);
-  else
-    return p.s.interleaved ? nr_launch_bwd<T, VEC, NV, true>(p, ctas, st)
-                           : nr_launch_bwd<T, VEC, NV, false>(p, ctas, st);
-}
-
-// The instance for a type, vector length and tasks per lane (see nr_vec and nr_tasks).
 template <typename Params>
 bool nr_run(const Params& p, int dtype, int vec, int nv, int ctas, cudaStream_t st) {
-  if (dtype == LOZA_FP32) {
-    if (vec == 4)
-      return nv == 1   ? nr_launch<float, 4, 1>(p, ctas, st)
-             : nv == 2 ? nr_launch<float, 4, 2>(p, ctas, st)
-                       : nr_launch<float, 4, 4>(p, ctas, st);
-    return nv == 4 ? nr_launch<float, 1, 4>(p, ctas, st) : nr_launch<float, 1, 16>(p, ctas, st);
-  }
-  auto half = [&](auto zero) {
-    using T = decltype(zero);
-    if (vec == 8) return nv == 1 ? nr_launch<T, 8, 1>(p, ctas, st) : nr_launch<T, 8, 2>(p, ctas, st);
-    if (vec == 2) return nv == 4 ? nr_launch<T, 2, 4>(p, ctas, st) : nr_launch<T, 2, 8>(p, ctas, st);
-    return nv == 4 ? nr_launch<T, 1, 4>(p, ctas, st) : nr_launch<T, 1, 16>(p, ctas, st);
-  };
-  return dtype == LOZA_BF16 ? half(__nv_bfloat16()) : half(__half());
+  return dtype == LOZA_FP32   ? nr_run_type<float>(p, vec, nv, ctas, st)
+         : dtype == LOZA_BF16 ? nr_run_type<__nv_bfloat16>(p, vec, nv, ctas, st)
+                              : nr_run_type<__half>(p, vec, nv, ctas, st);
 }
 
 // Warps that fill the GPU.
@@ -271,28 +192,6 @@ bool pkv_shape_ok(int32_t n_heads, int32_t n_kv, int32_t d_qk, int32_t d_v) {
 size_t pkv_part_o_bytes(int32_t d_v) { return (size_t)pkv_ctas() * 2 * kPkvHeads * d_v * sizeof(float); }
 size_t pkv_workspace_bytes(int32_t d_v) {
   return pkv_part_o_bytes(d_v) + (size_t)pkv_ctas() * (2 * kPkvHeads * 2 * sizeof(float) + sizeof(int4));
-}
-
-template <typename T, int DQK, int DV, int NT>
-loza_status pkv_launch(const PagedKvParams& p, cudaStream_t st) {
-  auto kernel = decode_paged_kv_kernel<T, DQK, DV, NT>;
-  constexpr int smem = PagedKvLayout<DQK, DV, NT>::kSmem;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return LOZA_ERR_CUDA;
-  kernel<<<(unsigned)p.ctas, kPkvThreads, smem, st>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return LOZA_ERR_CUDA;
-  if (!launch_after(decode_paged_join_kernel<T, DV>, dim3(p.ctas, p.chunk), 256, st, p))
-    return LOZA_ERR_CUDA;
-  g_launches.fetch_add(2, std::memory_order_relaxed);
-  return LOZA_OK;
-}
-
-template <typename T>
-loza_status pkv_dispatch(const PagedKvParams& p, int d_qk, cudaStream_t st) {
-  const bool wide = p.chunk > 8;  // more than one tile of 8 query heads
-  if (d_qk == 64) return wide ? pkv_launch<T, 64, 64, 2>(p, st) : pkv_launch<T, 64, 64, 1>(p, st);
-  if (d_qk == 128) return wide ? pkv_launch<T, 128, 128, 2>(p, st) : pkv_launch<T, 128, 128, 1>(p, st);
-  return wide ? pkv_launch<T, 192, 128, 2>(p, st) : pkv_launch<T, 192, 128, 1>(p, st);
 }
 
 }  // namespace
@@ -642,7 +541,9 @@ loza_status loza_ssa_decode_paged_kv(const loza_decode_paged_kv_args* args, loza
   p.ctas = pkv_ctas();
   p.split = reinterpret_cast<int4*>(p.part_ml + (size_t)p.ctas * 2 * kPkvHeads * 2);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return a.dtype == LOZA_BF16 ? pkv_dispatch<__nv_bfloat16>(p, a.d_qk, st) : pkv_dispatch<__half>(p, a.d_qk, st);
+  if (!(a.dtype == LOZA_BF16 ? pkv_run<__nv_bfloat16> : pkv_run<__half>)(p, a.d_qk, st)) return LOZA_ERR_CUDA;
+  g_launches.fetch_add(2, std::memory_order_relaxed);
+  return LOZA_OK;
 }
 
 }  // extern "C"
