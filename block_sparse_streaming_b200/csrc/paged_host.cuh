@@ -428,6 +428,9 @@ loza_status loza_qk_norm_rope_backward(const loza_qk_norm_rope_backward_args* ar
   if ((a.q_weight != nullptr) != (a.dq_weight != nullptr) || (a.k_weight != nullptr) != (a.dk_weight != nullptr))
     return LOZA_ERR_INVALID_ARG;
   if (!aligned_to(a.dq_weight, 4) || !aligned_to(a.dk_weight, 4)) return LOZA_ERR_INVALID_ARG;
+  if (a.dq_weight && a.dk_weight &&
+      overlap({a.dq_weight, (uint64_t)a.norm_dim * 4}, {a.dk_weight, (uint64_t)a.norm_dim * 4}))
+    return LOZA_ERR_INVALID_ARG;  // a weight of both sides has two gradients, which the caller adds
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a.tokens == 0) {  // the weights' gradients are sums over nothing
     if (a.dq_weight && cudaMemsetAsync(a.dq_weight, 0, (size_t)a.norm_dim * 4, st) != cudaSuccess) return LOZA_ERR_CUDA;

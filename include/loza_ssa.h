@@ -608,7 +608,8 @@ size_t loza_qk_norm_rope_workspace_size(int32_t norm_dim);
  * Gradient of loza_qk_norm_rope: from dq_out and dk_out (the gradients of
  * q_out and k_out) and the forward's inputs, dq, dk (same dtype) and the
  * weights' gradients dq_weight, dk_weight ([norm_dim] fp32, written, summed
- * over all tokens and heads; each given exactly if its weight is). A side
+ * over all tokens and heads; each given exactly if its weight is, and in memory
+ * of its own: the gradient of a weight of both sides is their sum). A side
  * without weight needs no q (k). The sums' order is fixed: no atomics, the
  * same bits every run on one kind of GPU. dq may replace dq_out or q, and dk
  * dk_out or k, with the same row strides.

@@ -3,7 +3,7 @@ that a kernel could not load from, and outputs that lie on inputs which other pa
 import pytest
 
 import block_sparse_streaming_b200 as bss
-from test_abi_paged import INVALID, _decode, _plan
+from test_abi_paged import INVALID, _bwd, _decode, _plan
 
 CTX, NEW, FREE, TABLE = 1 << 20, 1 << 21, 1 << 22, 1 << 23  # _plan's inputs: 4 requests, 9 free pages, 4 rows of 8
 
@@ -54,3 +54,8 @@ def test_plan_refuses_misaligned_pointers(L, over):
 @pytest.mark.parametrize("over", [dict(bt=(1 << 21) + 2), dict(lens=(1 << 22) + 1), dict(lse=(1 << 24) + 2)])
 def test_decode_refuses_misaligned_pointers(L, over):
     assert refused(L, _decode, **over)
+
+
+@pytest.mark.parametrize("over", [dict(dkw=1 << 30), dict(dkw=(1 << 30) + 4 * 127), dict(dkw=(1 << 30) - 4 * 127)])
+def test_backward_refuses_one_place_for_both_weights_gradients(L, over):
+    assert refused(L, _bwd, **over)
