@@ -142,21 +142,38 @@ int nr_batch(const NrShape& s, int warps, int wide_log) {
 // shares end up to 40 % apart: SMs do not get equal parts of the memory's
 // bandwidth (a pure copy's CTAs ended between 60 and 135 us). Short walks that
 // the hardware deals out as warps end even this out, but each starts with an
-// empty ring and angles to form, so a token must have groups enough. Equal
-// shares / short walks, us: rotation of 16,411 tokens, 64 heads of 192 (32
-// groups, walks of 1 token) 152 / 127, 16,384 tokens, 32 heads of 128 (8; 2)
-// 53 / 46, 32 + 8 heads of 128 without weights (12; 1) 77 / 64; with weights 12
-// groups (2) 76 / 73, 20 (1) 128 / 110, in fp32 24 (1) 152 / 127. Not with fewer:
-// rotation of 8 heads (2 groups) 59 / 65, 16 + 4 heads of 256 with weights (11)
-// 71 / 73, rows of 4-byte vectors 30 / 33; nor with less than one and a half
-// walks per warp that fits (1.05: 15 / 19).
+// empty ring and angles to form, so a token must have groups enough, and the
+// memory must be what the call waits for. Equal shares / short walks, us, of
+// 16,384 tokens unless said, groups of a token in brackets:
+// - One task a lane, rotation alone, from 8 groups: 64 heads of 192 (32) 152 /
+//   127, 32 heads of 128 (8) 52 / 46, of 64 heads of 64 (8) 52 / 45; fewer:
+//   16 heads of 128 (4) 24 / 30, 8 of 192 (4) 22 / 27, but 28 of 128 (7) 47 / 41.
+// - With weights, from 12: 32 + 8 heads of 128 (12) 76 / 74, 40 + 8 (14) 92 /
+//   84, 64 + 8 (20) 128 / 110, 64 + 64 of 192 (80), 8,192 tokens, 226 / 190, fp32
+//   32 + 8 of 64 (12) 79 / 68; fewer: 28 + 8 of 128 (11) 70 / 71, 16 + 4 of 256
+//   (11) 71 / 75, but fp32 14 + 4 of 128 (11) 74 / 67. Rows whose lanes or
+//   groups are not full pay for more than they load and lose 3-6 % up to some 20
+//   groups: 32 + 6 of 128 (12) 70 / 74, 32 + 8 of 192 (22) 118 / 123.
+// - Several tasks a lane (8 warps an SM), 8,192 tokens. Rotation alone: 12 heads
+//   of 576 (12) 44 / 39, 64 (64) 216 / 192, 8 (8) 29 / 30; every 32 pairs are
+//   a turn of the warp over the angles and want a group more: 16 of 1024, all
+//   rotated (16) 120 / 130, 32 (32) 207 / 194. Normed queries are bound by
+//   arithmetic: 16 + 1 heads of 576 (17) 90 / 106, 64 + 1 (65) 284 / 297; with
+//   few normed keys beside queries that are not, 48 + 1 (49) 172 / 153, but 24 + 1
+//   (25) 85 / 86, 32 + 8 (40) 137 / 144.
+// Nor with vectors of less than 16 bytes (30 / 33), nor with less than one and a
+// half walks per warp that fits (1.05: 15 / 19).
 void nr_plan_fwd(NrFwdParams* p, int vec, int nv, int size, int64_t groups, int64_t token_groups) {
   const int64_t warps = nr_warps(vec, nv);
   p->wide_log = nr_wide(p->s.tokens, groups, warps, 64);
   p->walks = (int)std::min(p->s.tokens, warps >> p->wide_log);
   p->batch = nr_batch(p->s, 1, p->wide_log);
   const bool norm = p->q.w || p->k.w;
-  if (vec * size == 16 && p->wide_log == 0 && token_groups >= (norm ? 12 : 8)) {
+  const int64_t rows = 32 >> p->s.lph_log, gq = (p->q.heads + rows - 1) / rows, gk = (p->k.heads + rows - 1) / rows;
+  const bool deal = nv == 1 ? token_groups >= (norm ? 12 : 8)
+                    : norm  ? !p->q.w && gq >= 8 * gk && token_groups >= 32
+                            : token_groups >= 11 + p->s.pairs / 32;
+  if (vec * size == 16 && p->wide_log == 0 && deal) {
     const int64_t least = norm ? 20 : 12;  // groups of a walk
     const int64_t walk = (least + token_groups - 1) / token_groups;
     const int64_t walks = (p->s.tokens + walk - 1) / walk;
