@@ -35,8 +35,8 @@
 // walk of many that are dealt out as warps end: see nr_plan_fwd), a CTA of the
 // gradient an equal share, in batches; the next batch's angles are formed in
 // shared memory, each once, before the current one's rows. Rows whose sizes,
-// offsets or strides are no multiple of 16 bytes run the same code with vectors
-// of 4 bytes or of one element.
+// offsets or strides, or half of whose rotated columns, are no multiple of 16
+// bytes run the same code with vectors of 4 bytes or of one element.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -544,9 +544,10 @@ loza_status loza_rope_frequencies(double theta, int32_t rope_dim, int32_t scalin
  * double [rope_dim / 2]. out may be x with the same stride (then only the
  * rotated columns are touched) or must not overlap it. transposed = 1 applies
  * the transposed map, which is the gradient: dx from dout. 32-bit arithmetic,
- * one rounding. Sizes, offsets, strides and pointers that are multiples of 16
- * bytes run in 16-byte vectors; others in vectors of 4 bytes or element by
- * element.
+ * one rounding. Where the head's size, rope_offset, HALF of rope_dim (and
+ * norm_dim below), strides and pointers are all multiples of 16 bytes, rows move
+ * in 16-byte vectors; else, for 16-bit types, in vectors of 4 bytes if they are
+ * all multiples of that, else element by element: two to five times as long.
  */
 typedef struct {
     const void *x;
@@ -657,6 +658,8 @@ size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, 
  *           seqlens[n] - 1. A sequence of length 0 (an idle row of a padded
  *           batch), or none of whose pages is there, gives out 0 and lse -inf
  *   Rows at or past seqlens[n], and rows outside the window, are not read.
+ *   An infinity or NaN in a visible row of v leaves NaN in its column, also
+ *   where the row's weight has underflowed to 0
  *   out     [batch, n_heads, d_v] of the same dtype; lse [batch, n_heads] fp32
  *   workspace  loza_decode_paged_kv_workspace_size(...) bytes, 16-byte
  *           aligned, contents on entry ignored; calls that can overlap on the
