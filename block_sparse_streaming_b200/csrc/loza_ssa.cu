@@ -48,7 +48,13 @@ EncodeTiledFn encode_fn() {
       return static_cast<EncodeTiledFn>(nullptr);
     return reinterpret_cast<EncodeTiledFn>(p);
   }();
-  return fn;
+  // The driver's function wants a current context. A host thread gets one from its first runtime call that needs it,
+  // which this may be (in torch.autograd's thread, whose memory comes from a cache, it is): bind the device's.
+  thread_local const bool bound = [] {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+  }();
+  return bound ? fn : nullptr;
 }
 
 // 3-D bf16 map over [rows, heads, dim] with 128-byte swizzle and a
