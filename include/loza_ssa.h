@@ -658,8 +658,8 @@ size_t loza_decode_paged_kv_workspace_size(int32_t n_heads, int32_t n_kv_heads, 
  *           seqlens[n] - 1. A sequence of length 0 (an idle row of a padded
  *           batch), or none of whose pages is there, gives out 0 and lse -inf
  *   Rows at or past seqlens[n], and rows outside the window, are not read.
- *   An infinity or NaN in a visible row of v leaves NaN in its column, also
- *   where the row's weight has underflowed to 0
+ *   An infinity or NaN in a visible row of v leaves an infinity or NaN in its
+ *   column, also where the row's weight has underflowed to 0
  *   out     [batch, n_heads, d_v] of the same dtype; lse [batch, n_heads] fp32
  *   workspace  loza_decode_paged_kv_workspace_size(...) bytes, 16-byte
  *           aligned, contents on entry ignored; calls that can overlap on the

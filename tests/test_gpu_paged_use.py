@@ -213,3 +213,20 @@ def test_pool_of_one_page_has_any_page_stride(bss):
     got = bss.loza_ssa_decode_paged_kv(q, *odd, table, lens, T, p)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(pools[1][0, :T], k)
+
+
+def test_infinite_values_stay_in_their_column(bss):
+    """An infinity in a visible value row spoils that column of its key head's queries and nothing else."""
+    B, H, Hk, d, P, L = 2, 8, 2, 64, 16, 100
+    dt = torch.bfloat16
+    q, k, v = normal(1, B, H, d, dtype=dt), normal(2, 16, P, Hk, d, dtype=dt), normal(3, 16, P, Hk, d, dtype=dt)
+    table = torch.arange(14, device="cuda", dtype=torch.int32).view(2, 7)
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    p = bss.Params(0.1, 128, 0, -1)
+    clean = bss.loza_ssa_decode_paged_kv(q, k, v, table, lens, L, p)
+    v[3, 5, 1, 17], v[8, 0, 0, 2] = float("inf"), float("nan")  # sequence 0, key head 1; sequence 1, key head 0
+    out, lse = bss.loza_ssa_decode_paged_kv(q, k, v, table, lens, L, p)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[0, 4:, 17], bad[1, :4, 2] = True, True
+    assert torch.equal(lse, clean[1]) and torch.equal(out[~bad], clean[0][~bad])
+    assert not torch.isfinite(out[bad]).any()
