@@ -422,14 +422,18 @@ __global__ void __launch_bounds__(kPkvThreads, kPkvCtasPerSm) decode_paged_kv_ke
         for (int k = 0; k < DV / 16; ++k) {
           uint32_t a[4];
           ldsm4_trans(a, vd + vr * (DV * 2) + (((2 * k + vc) ^ (vr & 7)) << 4));
+          float f[NT][4];  // of this step alone
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float f[4] = {0.f, 0.f, 0.f, 0.f};  // of this step alone
-            Mma16<T>::mma(f, a, pl[t][0], pl[t][1]);
-            Mma16<T>::mma(f, a, ph[t][0], ph[t][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][k][e] += f[e];
+            f[t][0] = f[t][1] = f[t][2] = f[t][3] = 0.f;
+            Mma16<T>::mma(f[t], a, pl[t][0], pl[t][1]);
           }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) Mma16<T>::mma(f[t], a, ph[t][0], ph[t][1]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][k][e] += f[t][e];
         }
       }
       st = st + 1 == S ? 0 : st + 1;
