@@ -7,9 +7,10 @@
 // Every visible K and V row is asked for once per up to 16 query heads and used
 // for 2 (d_qk + d_v) operations a head: at most 32 per byte, so up to 16 heads
 // on a key head HBM bounds it and the matrix instructions only have to stay out
-// of the way (16 heads on one, 64 sequences of 65,536: 348 us, 6.2 TB/s). Larger
+// of the way (16 heads on one, 64 sequences of 65,536: 317 us, 6.8 TB/s). Larger
 // groups read every row once per 16 heads, from HBM too (71 on one: 2.66 GB for
-// 0.54 GB of rows), and take as many times as long (32 on one 704 us, 71 1,825).
+// 0.54 GB of rows), and take as many times as long (32 on one 620-740 us, as the
+// parts of a sequence find each other's rows in L2 or not; 71 1,825).
 // Shapes: (d_qk, d_v) in {(64,64), (128,128), (192,128)}.
 //
 // Split. The work is cut into steps of 64 keys of one (sequence, key head,
