@@ -1241,10 +1241,12 @@ loza_status hi_select_launch(const void* q_index, const void* k_index, int64_t i
   hp.tok_cand = reinterpret_cast<unsigned long long*>(ws + w.tok_cand);
   hp.selected = selected;
   hp.n_sel = reinterpret_cast<int32_t*>(ws + w.n_sel);
+  // limits of the context, which another thread's call may set before this one launches: the same from every call
+  static_assert(HiTopkLayout::bytes(kHiMaxPages) <= 227 * 1024, "shared memory of a CTA");
   if (cudaFuncSetAttribute(hi_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            HiTokLayout::SMEM_ALLOC) != cudaSuccess ||
       cudaFuncSetAttribute(hi_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           HiTopkLayout::bytes(hp.pages_per_seq)) != cudaSuccess)
+                           HiTopkLayout::bytes(kHiMaxPages)) != cudaSuccess)
     return LOZA_ERR_CUDA;
   if (cudaMemsetAsync(ws + w.zeroed, 0, w.zeroed_bytes, st) != cudaSuccess) return LOZA_ERR_CUDA;
   int launches = 4;
